@@ -47,38 +47,10 @@
 // of the same code, in 256-thread workgroups without the cap; the read-only
 // gradient may sit at any 4-byte boundary and the write-only output (bf16
 // re-cast, ZeRO-1 update) at any element offset on the vector path.
-#include "zs_common.h"
+#include "adamw_math.h"
 
 namespace zs {
 namespace {
-
-// One element: the moments in place and the returned step u, in the order
-// and with the roundings the header documents.  Built with
-// -ffp-contract=off: no multiply-add fusion; the quotient and square root
-// are IEEE round-to-nearest (correctly rounded fp32 division and sqrt are
-// requested at compile time).
-__device__ __forceinline__ float adam_elem(const AdamwScalars& a, float coef, float gr, float& m, float& v) {
-    float g = gr * a.grad_scale;
-    g = g * coef;
-    const float m_keep = a.beta1 * m;
-    const float m_new = a.one_minus_beta1 * g;
-    m = m_keep + m_new;
-    const float g2 = g * g;
-    const float v_keep = a.beta2 * v;
-    const float v_new = a.one_minus_beta2 * g2;
-    v = v_keep + v_new;
-    const float root = sqrtf(v);
-    float den = root / a.bias_correction2_sqrt;
-    den = den + a.eps;
-    const float ratio = m / den;
-    return ratio * a.step_size;
-}
-
-// the parameter after the step: decoupled decay, then the step
-__device__ __forceinline__ float apply_step(const AdamwScalars& a, float p, float u) {
-    const float pd = p * a.decay;
-    return pd - u;
-}
 
 // Four consecutive gradient elements from `first` (vector path; every source
 // is read-only, so dword alignment suffices) and one element (scalar path),
@@ -110,23 +82,6 @@ __device__ __forceinline__ float grad1(const AdamwArgs& a, int64_t i) {
         if constexpr (GS == kGradBf16) return g;
         else return a.grad[i] + g;
     }
-}
-
-// Clip coefficient from the squared norm, in binary64 (uniform per wave).
-// Returns false when the global squared norm is not finite: the step is
-// skipped, no state is written (the update form writes -0.0, see below).
-__device__ __forceinline__ bool clip_coef(const AdamwScalars& a, const double* norm_sq, float& coef) {
-    coef = 1.0f;
-    if (norm_sq == nullptr) return true;
-    const double s = *norm_sq + a.extra_norm_sq;
-    if (!__builtin_isfinite(s)) return false;
-    if (a.clip) {
-        const double total = sqrt(s);
-        double c = a.max_norm / (total + 1e-6);
-        if (c > 1.0) c = 1.0;
-        coef = (float)c;
-    }
-    return true;
 }
 
 // A skipped ZeRO-1 step (non-finite global norm) still writes its update
