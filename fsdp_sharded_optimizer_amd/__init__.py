@@ -32,6 +32,15 @@ The Python names mirror the C ABI in include/zshard.h:
     adam_update_tiled(hp, moments, grad, update, norm_sq=None)
     adamw_step_no_master_tiled(hp, param_bf16, moments, grad, norm_sq=None)
 
+Over lists of tensors (include/zshard_tensors.h), each list marshalled once:
+
+    GradTensors(grads) / AdamWTensors(params, grads, exp_avg, exp_avg_sq, param_bf16=None)
+    AdamWQ8Tensors(params, grads, states, param_bf16=None) / Q8Moments(states, exp_avg, exp_avg_sq)
+    grad_norm_sq_tensors(grads, grad_scale, out, workspace=None)
+    adamw_step_tensors(hp, tensors, norm_sq=None)               fp32 moments; _dev: scalars in device memory
+    adamw_step_tensors_q8(hp, tensors, seed=0, norm_sq=None)    8-bit moments; _dev: q8_scalars_bytes(hp, seed)
+    moments_q8_bytes(n) / moments_q8_encode(moments, seed=0) / moments_q8_decode(moments)
+
 DeviceArena(nbytes, device) holds one physically contiguous block of device
 memory and hands out 2 MiB-aligned views of it (ShardOptimizer(arena=...)).
 
@@ -84,3 +93,22 @@ from ._binding import (  # noqa: F401
 )
 from .arena import DeviceArena  # noqa: F401
 from .step import ShardOptimizer  # noqa: F401
+from .tensors import (  # noqa: F401
+    Q8_BLOCK,
+    TENSOR_EXPORTS,
+    AdamWQ8Scalars,
+    AdamWQ8Tensors,
+    AdamWTensors,
+    GradTensors,
+    Q8Moments,
+    adamw_step_tensors,
+    adamw_step_tensors_dev,
+    adamw_step_tensors_q8,
+    adamw_step_tensors_q8_dev,
+    grad_norm_sq_tensors,
+    grad_norm_sq_tensors_workspace_bytes,
+    moments_q8_bytes,
+    moments_q8_decode,
+    moments_q8_encode,
+    q8_scalars_bytes,
+)

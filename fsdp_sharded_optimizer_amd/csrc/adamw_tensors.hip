@@ -1,0 +1,92 @@
+// AdamW over a list of tensors with fp32 moments.
+//
+// The update of one element is adamw.hip's (adamw_math.h: the same operations
+// and roundings, so a tensor gets the bits adamw_step or adamw_step_no_master
+// would give it); here one launch covers up to 64 tensors of any sizes.
+// HBM-bound: with fp32 parameters 24 B/element of parameter and moments plus
+// the gradient (2 or 4) and the bf16 re-cast (2); with bf16 parameters 20 plus
+// the gradient.
+//
+// Layout: the flat step's: one-wave workgroups of 256 elements, 4 consecutive
+// per lane, a 128-bit access per fp32 stream (64-bit per bf16 one), residency
+// capped by reserved LDS.  A workgroup's tile lies in one tensor (find_tensor).
+#include "adamw_math.h"
+#include "tensors.h"
+
+namespace zs {
+namespace {
+
+constexpr int kWave = 64;
+constexpr unsigned kLds = 16384;
+
+template <bool PBF16, bool GBF16, bool DEV>
+__global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b) {
+    using P = typename GradType<PBF16>::T;
+    using G = typename GradType<GBF16>::T;
+    uint32_t first;
+    const int t = find_tensor(b.tab, blockIdx.x, first);
+    const AdamwEntry& e = b.e[t];
+    const AdamwScalars sc = DEV ? *b.sc_dev : b.sc;
+    P* const param = static_cast<P*>(e.param);
+    const G* const grad = static_cast<const G*>(e.grad);
+    const int64_t n = e.numel;
+    const int64_t i = (int64_t)(blockIdx.x - first) * kListTile - e.shift + threadIdx.x * 4;
+    float coef;
+    if (i >= 0 && i + 4 <= n) {
+        // the loads are issued before the clip coefficient is resolved
+        const f32x4 g4 = ld4(grad + i);
+        f32x4 p4 = ld4(param + i);
+        f32x4 m4 = ld4(e.exp_avg + i);
+        f32x4 v4 = ld4(e.exp_avg_sq + i);
+        if (!clip_coef(sc, b.norm_sq, coef)) return;
+        float gs[4] = {g4.x, g4.y, g4.z, g4.w};
+        float ps[4] = {p4.x, p4.y, p4.z, p4.w};
+        float ms[4] = {m4.x, m4.y, m4.z, m4.w};
+        float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float u = adam_elem(sc, coef, gs[j], ms[j], vs[j]);
+            ps[j] = apply_step(sc, ps[j], u);
+        }
+        const f32x4 po = {ps[0], ps[1], ps[2], ps[3]};
+        st4(param + i, po);
+        st4(e.exp_avg + i, f32x4{ms[0], ms[1], ms[2], ms[3]});
+        st4(e.exp_avg_sq + i, f32x4{vs[0], vs[1], vs[2], vs[3]});
+        if (!PBF16 && e.copy != nullptr) st4(e.copy + i, po);
+        return;
+    }
+    // lanes across a tensor's start or end (or outside it)
+    if (!clip_coef(sc, b.norm_sq, coef)) return;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const int64_t k = i + j;
+        if (k < 0 || k >= n) continue;
+        float m = e.exp_avg[k], v = e.exp_avg_sq[k];
+        const float u = adam_elem(sc, coef, widen(grad[k]), m, v);
+        const float p = apply_step(sc, widen(param[k]), u);
+        st1(param + k, p);
+        e.exp_avg[k] = m;
+        e.exp_avg_sq[k] = v;
+        if (!PBF16 && e.copy != nullptr) st1(e.copy + k, p);
+    }
+}
+
+template <bool PBF16, bool GBF16>
+hipError_t launch(const AdamwBatch& b, int64_t tiles, hipStream_t stream) {
+    const dim3 grid((unsigned)tiles), block(kWave);
+    if (b.sc_dev != nullptr)
+        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, true>), grid, block, kLds, stream, b);
+    else
+        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, false>), grid, block, kLds, stream, b);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, int64_t tiles,
+                                hipStream_t stream) {
+    if (param_bf16) return grad_bf16 ? launch<true, true>(b, tiles, stream) : launch<true, false>(b, tiles, stream);
+    return grad_bf16 ? launch<false, true>(b, tiles, stream) : launch<false, false>(b, tiles, stream);
+}
+
+}  // namespace zs

@@ -1,0 +1,418 @@
+// C-ABI entry points over lists of tensors (include/zshard_tensors.h):
+// validation on the host, then launches of up to 64 tensors each.
+#include <algorithm>
+#include <cstddef>
+#include <cstdlib>
+
+#include "../../include/zshard_tensors.h"
+#include "api_common.h"
+#include "q8.h"
+#include "reduce.h"
+
+using namespace zs;
+
+static_assert(ZS_Q8_BLOCK == kQ8Block, "block length of the header and the kernels");
+static_assert(sizeof(zs_adamw_q8_scalars) == sizeof(Q8Scalars) &&
+                  offsetof(zs_adamw_q8_scalars, key) == offsetof(Q8Scalars, key), "scalar layout");
+static_assert(kLaunchElems % kQ8Pad == 0 && kLaunchElems % kListTile == 0, "pieces start on a tile");
+
+namespace {
+
+// The byte ranges of one call, and whether any written one shares a byte with
+// another.  Sorted by address: O(k log k), since a list of some hundred
+// tensors has thousands of buffers (pairwise, milliseconds).
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+};
+
+struct Ranges {
+    Range* r = nullptr;
+    int64_t count = 0;
+    Range few[512];
+
+    // false: no memory for the table
+    bool reserve(int64_t most) {
+        r = most <= (int64_t)(sizeof(few) / sizeof(few[0])) ? few : static_cast<Range*>(std::malloc(most * sizeof(Range)));
+        return r != nullptr;
+    }
+    ~Ranges() {
+        if (r != few) std::free(r);
+    }
+    void add(const void* p, int64_t bytes, bool written) {
+        if (p != nullptr && bytes > 0) r[count++] = Range{addr(p), addr(p) + (uintptr_t)bytes, written};
+    }
+    bool clash() {
+        std::sort(r, r + count, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        uintptr_t written_to = 0, any_to = 0;   // how far the ranges before this one reach
+        for (int64_t i = 0; i < count; ++i) {
+            if (r[i].lo < written_to || (r[i].written && r[i].lo < any_to)) return true;
+            any_to = std::max(any_to, r[i].hi);
+            if (r[i].written) written_to = std::max(written_to, r[i].hi);
+        }
+        return false;
+    }
+};
+
+// The sum of the list's numels, or -1 for a bad list.
+template <typename T>
+int64_t list_total(const T* list, int32_t count) {
+    if (count < 0 || (count > 0 && list == nullptr)) return -1;
+    int64_t total = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        if (!size_ok(list[k].numel) || total > kMaxElems - list[k].numel) return -1;
+        total += list[k].numel;
+    }
+    return total;
+}
+
+// Fills launches with entries: `launch(batch, tiles)` for each full table.
+template <typename Batch, typename Launch>
+class Filler {
+public:
+    Filler(Batch& b, Launch launch) : b_(b), launch_(launch) { clear(); }
+    // room for an entry of `tiles` workgroups; the entry's place in out
+    int32_t add(int64_t tiles, int& out) {
+        if (count_ == kListMax || tiles_ + tiles > kListMaxTiles) {
+            const int32_t rc = flush();
+            if (rc != ZS_OK) return rc;
+        }
+        out = count_;
+        b_.tab.tile_start[count_] = (uint32_t)tiles_;
+        if (count_ % kListGroup == 0) b_.tab.coarse[count_ / kListGroup] = (uint32_t)tiles_;
+        ++count_;
+        tiles_ += tiles;
+        return ZS_OK;
+    }
+    int32_t flush() {
+        if (count_ == 0) return ZS_OK;
+        const int32_t rc = hip_status(launch_(b_, tiles_));
+        clear();
+        return rc;
+    }
+
+private:
+    void clear() {
+        std::memset(&b_.tab, 0xFF, sizeof(b_.tab));
+        count_ = 0;
+        tiles_ = 0;
+    }
+    Batch& b_;
+    Launch launch_;
+    int count_ = 0;
+    int64_t tiles_ = 0;
+};
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T>
+T* advance(T* p, int64_t bytes) {
+    return p == nullptr ? nullptr : reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
+}
+
+// Elements to start before a tensor's first one so that, after them, every
+// stream that is read and written is on a cache line (offsets in elements from
+// a line agree across the streams); 0 where they do already or do not agree.
+// A read-modify-write stream whose waves share lines runs a quarter slower.
+constexpr int64_t kLine = 128;
+int64_t line_shift(const zs_adamw_tensor& t, int64_t psz) {
+    const int64_t per = kLine / psz;   // elements of param in a line (64 bf16 or 32 fp32)
+    const int64_t off = (int64_t)(addr(t.param) % kLine) / psz;
+    for (const float* s : {t.exp_avg, t.exp_avg_sq})
+        if ((int64_t)(addr(s) % kLine) / 4 != off % 32) return 0;
+    return off == 0 ? 0 : kListTile - (per - off);
+}
+
+int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const zs_adamw_tensor* list, int32_t count,
+                     int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev, void* hip_stream) {
+    const int64_t total = list_total(list, count);
+    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return ZS_EINVAL;
+    if (sc_dev == nullptr) {
+        const int32_t rc = adamw_check_hp(hp, total, norm_sq_dev);
+        if (rc != ZS_OK) return rc;
+    } else if (!aligned(sc_dev, 8) || (norm_sq_dev != nullptr && !aligned(norm_sq_dev, 8))) {
+        return ZS_EINVAL;
+    }
+    const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
+    Ranges ranges;
+    if (!ranges.reserve((int64_t)count * 5 + 2)) return ZS_EINVAL;
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_adamw_tensor& t = list[k];
+        if (t.numel == 0) continue;
+        if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr) return ZS_EINVAL;
+        if (!aligned(t.param, (uintptr_t)psz) || !aligned(t.grad, (uintptr_t)gsz) || !aligned(t.exp_avg, 4) ||
+            !aligned(t.exp_avg_sq, 4))
+            return ZS_EINVAL;
+        if (t.param_bf16 != nullptr && (param_dtype == ZS_BF16 || !aligned(t.param_bf16, 2))) return ZS_EINVAL;
+        ranges.add(t.param, t.numel * psz, true);
+        ranges.add(t.grad, t.numel * gsz, false);
+        ranges.add(t.exp_avg, t.numel * 4, true);
+        ranges.add(t.exp_avg_sq, t.numel * 4, true);
+        ranges.add(t.param_bf16, t.numel * 2, true);
+    }
+    ranges.add(norm_sq_dev, 8, false);
+    ranges.add(sc_dev, (int64_t)sizeof(zs_adamw_scalars), false);
+    if (ranges.clash()) return ZS_EOVERLAP;
+
+    AdamwBatch b;
+    std::memset(&b, 0, sizeof(b));
+    if (sc_dev == nullptr) b.sc = make_scalars(hp);
+    b.sc_dev = reinterpret_cast<const AdamwScalars*>(sc_dev);
+    b.norm_sq = norm_sq_dev;
+    auto launch = [&](const AdamwBatch& x, int64_t tiles) {
+        return launch_adamw_tensors(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, tiles, as_stream(hip_stream));
+    };
+    Filler<AdamwBatch, decltype(launch)> fill(b, launch);
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_adamw_tensor& t = list[k];
+        const int64_t shift = t.numel == 0 ? 0 : line_shift(t, psz);
+        for (int64_t off = 0; off < t.numel; off += kLaunchElems) {
+            const int64_t n = launch_piece(t.numel, off);
+            int at = 0;
+            const int32_t rc = fill.add(ceil_div(n + shift, kListTile), at);
+            if (rc != ZS_OK) return rc;
+            AdamwEntry& e = b.e[at];
+            e.param = advance(t.param, off * psz);
+            e.grad = advance(t.grad, off * gsz);
+            e.exp_avg = t.exp_avg + off;
+            e.exp_avg_sq = t.exp_avg_sq + off;
+            e.copy = advance(t.param_bf16, off * 2);
+            e.numel = (uint32_t)n;
+            e.shift = (uint32_t)shift;
+        }
+    }
+    return fill.flush();
+}
+
+uint32_t q8_key(uint32_t seed, int64_t step) { return q8_mix(q8_mix(seed) + (uint32_t)step); }
+
+// the entries of one tensor's pieces; `set(entry, element offset)` fills the pointers
+template <typename Fill, typename Set>
+int32_t add_q8(Q8Batch& b, Fill& fill, void* state, int64_t numel, uint32_t index, int64_t tile, Set set) {
+    for (int64_t off = 0; off < numel; off += kLaunchElems) {
+        const int64_t n = launch_piece(numel, off);
+        int at = 0;
+        const int32_t rc = fill.add(ceil_div(n, tile), at);
+        if (rc != ZS_OK) return rc;
+        Q8Entry& e = b.e[at];
+        std::memset(&e, 0, sizeof(e));
+        e.state = static_cast<uint8_t*>(state);
+        e.numel = (uint32_t)n;
+        e.off = (uint32_t)(off / kQ8Pad);
+        e.padded = (uint32_t)(q8_padded(numel) / kQ8Pad);
+        e.index = index;
+        set(e, off);
+    }
+    return ZS_OK;
+}
+
+int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_scalars* sc_dev,
+                        const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
+                        const double* norm_sq_dev, void* hip_stream) {
+    const int64_t total = list_total(list, count);
+    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return ZS_EINVAL;
+    if (sc_dev == nullptr) {
+        const int32_t rc = adamw_check_hp(hp, total, norm_sq_dev);
+        if (rc != ZS_OK) return rc;
+    } else if (!aligned(sc_dev, 8) || (norm_sq_dev != nullptr && !aligned(norm_sq_dev, 8))) {
+        return ZS_EINVAL;
+    }
+    const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
+    Ranges ranges;
+    if (!ranges.reserve((int64_t)count * 4 + 2)) return ZS_EINVAL;
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_adamw_q8_tensor& t = list[k];
+        if (t.numel == 0) continue;
+        if (t.param == nullptr || t.grad == nullptr || t.state_q8 == nullptr) return ZS_EINVAL;
+        if (!aligned(t.param, (uintptr_t)psz) || !aligned(t.grad, (uintptr_t)gsz) || !aligned(t.state_q8, 16))
+            return ZS_EINVAL;
+        if (t.param_bf16 != nullptr && (param_dtype == ZS_BF16 || !aligned(t.param_bf16, 2))) return ZS_EINVAL;
+        ranges.add(t.param, t.numel * psz, true);
+        ranges.add(t.grad, t.numel * gsz, false);
+        ranges.add(t.state_q8, moments_q8_bytes(t.numel), true);
+        ranges.add(t.param_bf16, t.numel * 2, true);
+    }
+    ranges.add(norm_sq_dev, 8, false);
+    ranges.add(sc_dev, (int64_t)sizeof(zs_adamw_q8_scalars), false);
+    if (ranges.clash()) return ZS_EOVERLAP;
+
+    Q8Batch b;
+    std::memset(&b, 0, sizeof(b));
+    if (sc_dev == nullptr) {
+        b.sc.adamw = make_scalars(hp);
+        b.sc.key = q8_key(seed, hp->step);
+    }
+    b.sc_dev = reinterpret_cast<const Q8Scalars*>(sc_dev);
+    b.norm_sq = norm_sq_dev;
+    auto launch = [&](const Q8Batch& x, int64_t tiles) {
+        return launch_adamw_q8(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, tiles, as_stream(hip_stream));
+    };
+    Filler<Q8Batch, decltype(launch)> fill(b, launch);
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_adamw_q8_tensor& t = list[k];
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, q8_step_tile(), [&](Q8Entry& e, int64_t off) {
+            e.param = advance(t.param, off * psz);
+            e.grad = advance(t.grad, off * gsz);
+            e.copy = advance(t.param_bf16, off * 2);
+        });
+        if (rc != ZS_OK) return rc;
+    }
+    return fill.flush();
+}
+
+// both conversions: encode reads the moments and writes the state, decode the reverse
+int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool encode, uint32_t seed,
+                   void* hip_stream) {
+    if (list_total(list, count) < 0 || !dtype_ok(dtype)) return ZS_EINVAL;
+    const int64_t sz = elem_size(dtype);
+    Ranges ranges;
+    if (!ranges.reserve((int64_t)count * 3)) return ZS_EINVAL;
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_moments_q8& t = list[k];
+        if (t.numel == 0) continue;
+        if (t.state_q8 == nullptr || !aligned(t.state_q8, 16)) return ZS_EINVAL;
+        for (void* p : {t.exp_avg, t.exp_avg_sq}) {
+            if (!aligned(p, (uintptr_t)sz)) return ZS_EINVAL;
+            ranges.add(p, t.numel * sz, !encode);
+        }
+        ranges.add(t.state_q8, moments_q8_bytes(t.numel), encode);
+    }
+    if (ranges.clash()) return ZS_EOVERLAP;
+    Q8Batch b;
+    std::memset(&b, 0, sizeof(b));
+    b.sc.key = q8_key(seed, 0);
+    auto launch = [&](const Q8Batch& x, int64_t tiles) {
+        return encode ? launch_q8_encode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream))
+                      : launch_q8_decode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream));
+    };
+    Filler<Q8Batch, decltype(launch)> fill(b, launch);
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_moments_q8& t = list[k];
+        if (!encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr) continue;
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, q8_codec_tile(), [&](Q8Entry& e, int64_t off) {
+            e.param = advance(t.exp_avg, off * sz);
+            void* const v = advance(t.exp_avg_sq, off * sz);
+            if (encode) e.grad = v;
+            else e.copy = v;
+        });
+        if (rc != ZS_OK) return rc;
+    }
+    return fill.flush();
+}
+
+// partials of the whole list, tensor after tensor; -1 for a bad list
+int64_t norm_partials_of(const zs_tensor* grads, int32_t count, int32_t grad_dtype) {
+    if (list_total(grads, count) < 0 || !dtype_ok(grad_dtype)) return -1;
+    const int64_t tile = norm_tile_elems(grad_dtype == ZS_BF16);
+    int64_t parts = 0;
+    for (int32_t k = 0; k < count; ++k) parts += ceil_div(grads[k].numel, tile);
+    return parts;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t grad_norm_sq_tensors_workspace_bytes(const zs_tensor* grads, int32_t count, int32_t grad_dtype) {
+    const int64_t parts = norm_partials_of(grads, count, grad_dtype);
+    if (parts < 0) return -1;
+    return (parts <= kSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
+}
+
+int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad_dtype, double grad_scale,
+                             double* out_sq_dev, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+    const int64_t parts = norm_partials_of(grads, count, grad_dtype);
+    if (parts < 0 || out_sq_dev == nullptr || !aligned(out_sq_dev, 8)) return ZS_EINVAL;
+    if (!(grad_scale > 0.0) || !std::isfinite(grad_scale)) return ZS_EINVAL;
+    const int64_t gsz = elem_size(grad_dtype);
+    const int64_t need = grad_norm_sq_tensors_workspace_bytes(grads, count, grad_dtype);
+    if (need > 0 && (workspace == nullptr || !aligned(workspace, 8))) return ZS_EINVAL;
+    if (workspace_bytes < need) return ZS_EWORKSPACE;
+    Ranges ranges;
+    if (!ranges.reserve((int64_t)count + 2)) return ZS_EINVAL;
+    for (int32_t k = 0; k < count; ++k) {
+        const zs_tensor& t = grads[k];
+        if (t.numel == 0) continue;
+        if (t.ptr == nullptr || !aligned(t.ptr, (uintptr_t)gsz)) return ZS_EINVAL;
+        ranges.add(t.ptr, t.numel * gsz, false);
+    }
+    ranges.add(out_sq_dev, 8, true);
+    ranges.add(workspace, need, true);
+    if (ranges.clash()) return ZS_EOVERLAP;
+
+    double* const partials = static_cast<double*>(workspace);
+    int64_t done = 0;   // partials of the launches before
+    NormBatch b;
+    std::memset(&b, 0, sizeof(b));
+    auto launch = [&](const NormBatch& x, int64_t tiles) {
+        const hipError_t e = launch_norm_tensors(x, grad_dtype == ZS_BF16, tiles, (float)grad_scale, partials + done,
+                                                 as_stream(hip_stream));
+        done += tiles;
+        return e;
+    };
+    Filler<NormBatch, decltype(launch)> fill(b, launch);
+    const int64_t tile = norm_tile_elems(grad_dtype == ZS_BF16);
+    for (int32_t k = 0; k < count; ++k)
+        for (int64_t off = 0; off < grads[k].numel; off += kLaunchElems) {
+            const int64_t n = launch_piece(grads[k].numel, off);
+            int at = 0;
+            const int32_t rc = fill.add(ceil_div(n, tile), at);
+            if (rc != ZS_OK) return rc;
+            b.e[at].grad = advance(grads[k].ptr, off * gsz);
+            b.e[at].numel = n;
+        }
+    const int32_t rc = fill.flush();
+    if (rc != ZS_OK) return rc;
+    return hip_status(launch_sum_partials(partials, parts, partials + parts, out_sq_dev, as_stream(hip_stream)));
+}
+
+int32_t adamw_step_tensors(const zs_adamw* hp, const zs_adamw_tensor* tensors, int32_t count, int32_t param_dtype,
+                           int32_t grad_dtype, const double* norm_sq_dev, void* hip_stream) {
+    if (hp == nullptr) return ZS_EINVAL;
+    return step_tensors(hp, nullptr, tensors, count, param_dtype, grad_dtype, norm_sq_dev, hip_stream);
+}
+
+int32_t adamw_step_tensors_dev(const zs_adamw_scalars* scalars_dev, const zs_adamw_tensor* tensors, int32_t count,
+                               int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev, void* hip_stream) {
+    if (scalars_dev == nullptr) return ZS_EINVAL;
+    return step_tensors(nullptr, scalars_dev, tensors, count, param_dtype, grad_dtype, norm_sq_dev, hip_stream);
+}
+
+int64_t moments_q8_bytes(int64_t n) {
+    if (!size_ok(n)) return -1;
+    const int64_t p = q8_padded(n);
+    return ceil_div(2 * p + p / (kQ8Block / 2), kLine) * kLine;
+}
+
+int32_t moments_q8_encode(const zs_moments_q8* moments, int32_t count, int32_t dtype, uint32_t seed,
+                          void* hip_stream) {
+    return convert_q8(moments, count, dtype, true, seed, hip_stream);
+}
+
+int32_t moments_q8_decode(const zs_moments_q8* moments, int32_t count, int32_t dtype, void* hip_stream) {
+    return convert_q8(moments, count, dtype, false, 0, hip_stream);
+}
+
+int32_t adamw_step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_tensor* tensors, int32_t count,
+                              int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev, void* hip_stream) {
+    if (hp == nullptr) return ZS_EINVAL;
+    return step_tensors_q8(hp, seed, nullptr, tensors, count, param_dtype, grad_dtype, norm_sq_dev, hip_stream);
+}
+
+int32_t adamw_q8_scalars(const zs_adamw* hp, uint32_t seed, zs_adamw_q8_scalars* out) {
+    if (out == nullptr) return ZS_EINVAL;
+    const int32_t rc = adamw_scalars(hp, &out->adamw);
+    if (rc != ZS_OK) return rc;
+    out->key = q8_key(seed, hp->step);
+    out->reserved = 0;
+    return ZS_OK;
+}
+
+int32_t adamw_step_tensors_q8_dev(const zs_adamw_q8_scalars* scalars_dev, const zs_adamw_q8_tensor* tensors,
+                                  int32_t count, int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev,
+                                  void* hip_stream) {
+    if (scalars_dev == nullptr) return ZS_EINVAL;
+    return step_tensors_q8(nullptr, 0, scalars_dev, tensors, count, param_dtype, grad_dtype, norm_sq_dev, hip_stream);
+}
+
+}  // extern "C"

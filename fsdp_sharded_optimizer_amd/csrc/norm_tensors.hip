@@ -1,0 +1,86 @@
+// The squared global norm of a list of gradients.
+//
+// sum (double)fl32(widen(g) * scale)^2 over every tensor, in binary64: each
+// workgroup adds the squares of one tile of one tensor (zs::add_squares4, the
+// butterfly and LDS order of reduce.h) and writes one partial; the partials
+// are added by the fixed tree of launch_sum_partials.  The association depends
+// only on the numels, the dtype and their order.  HBM-bound: 4 (2) bytes per
+// element, read once.
+//
+// Layout: the standalone norm's (norm.hip): 256-thread workgroups, four
+// lane-contiguous 128-bit loads per lane (4096 fp32 or 8192 bf16 elements),
+// all issued before the first square, 24 KiB of LDS reserved (6 workgroups
+// per CU).  The gradients are only read, so they are loaded 128 bits wide at
+// any element alignment.
+#include "reduce.h"
+#include "tensors.h"
+
+namespace zs {
+namespace {
+
+constexpr int kQ = 4;
+constexpr unsigned kLds = 24576;
+template <bool BF16> constexpr int kVec = BF16 ? 8 : 4;   // elements of a 128-bit load
+template <bool BF16> constexpr int64_t kTile = (int64_t)kBlock * kVec<BF16> * kQ;
+
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b, float scale,
+                                                              double* __restrict__ partials) {
+    constexpr int VE = kVec<BF16>;
+    using T = typename GradType<BF16>::T;
+    uint32_t first;
+    const int t = find_tensor(b.tab, blockIdx.x, first);
+    const T* const grad = static_cast<const T*>(b.e[t].grad);
+    const int64_t n = b.e[t].numel;
+    const int64_t tile = (int64_t)(blockIdx.x - first) * kTile<BF16>;
+    const int64_t lane0 = tile + threadIdx.x * VE;
+    double s0 = 0.0, s1 = 0.0;
+    if (tile + kTile<BF16> <= n) {
+        u32x4 v[kQ];
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) v[q] = ld_stream_u32x4_any(grad + lane0 + q * kBlock * VE);
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            if constexpr (BF16) {
+                const float lo[4] = {bf16_to_f32(v[q].x & 0xFFFFu), bf16_to_f32(v[q].x >> 16),
+                                     bf16_to_f32(v[q].y & 0xFFFFu), bf16_to_f32(v[q].y >> 16)};
+                const float hi[4] = {bf16_to_f32(v[q].z & 0xFFFFu), bf16_to_f32(v[q].z >> 16),
+                                     bf16_to_f32(v[q].w & 0xFFFFu), bf16_to_f32(v[q].w >> 16)};
+                add_squares4(lo, scale, s0, s1);
+                add_squares4(hi, scale, s0, s1);
+            } else {
+                const float g[4] = {__uint_as_float(v[q].x), __uint_as_float(v[q].y), __uint_as_float(v[q].z),
+                                    __uint_as_float(v[q].w)};
+                add_squares4(g, scale, s0, s1);
+            }
+        }
+    } else {   // a tensor's ragged last tile: elements past the end add +0
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int h = 0; h < VE; h += 4) {
+                const int64_t at = lane0 + q * kBlock * VE + h;
+                float g[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[j] = at + j < n ? widen(grad[at + j]) : 0.0f;
+                add_squares4(g, scale, s0, s1);
+            }
+    }
+    const double total = block_sum(s0 + s1);
+    if (threadIdx.x == 0) partials[xcd_slot(blockIdx.x, gridDim.x)] = total;
+}
+
+}  // namespace
+
+int64_t norm_tile_elems(int grad_bf16) { return grad_bf16 ? kTile<true> : kTile<false>; }
+
+hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, int64_t tiles, float scale, double* partials,
+                               hipStream_t stream) {
+    static_assert(kLaunchElems % kTile<true> == 0, "pieces of a tensor keep its tiles");
+    const dim3 grid((unsigned)tiles), block(kBlock);
+    if (grad_bf16) hipLaunchKernelGGL(norm_tensors_kernel<true>, grid, block, kLds, stream, b, scale, partials);
+    else hipLaunchKernelGGL(norm_tensors_kernel<false>, grid, block, kLds, stream, b, scale, partials);
+    return hipGetLastError();
+}
+
+}  // namespace zs
