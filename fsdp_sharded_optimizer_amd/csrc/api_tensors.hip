@@ -250,7 +250,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, q8_step_tile(), [&](Q8Entry& e, int64_t off) {
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, kQ8Pad, [&](Q8Entry& e, int64_t off) {
             e.param = advance(t.param, off * psz);
             e.grad = advance(t.grad, off * gsz);
             e.copy = advance(t.param_bf16, off * 2);
@@ -289,7 +289,7 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
         if (!encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr) continue;
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, q8_codec_tile(), [&](Q8Entry& e, int64_t off) {
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, kQ8Pad, [&](Q8Entry& e, int64_t off) {
             e.param = advance(t.exp_avg, off * sz);
             void* const v = advance(t.exp_avg_sq, off * sz);
             if (encode) e.grad = v;

@@ -1,10 +1,15 @@
 // AdamW over a list of tensors with 8-bit moments, and the conversions of
 // such moments.
 //
-// The step decodes a block's moments, forms the new ones and the parameter as
-// the fp32 step does (adamw_math.h), takes the block's two new scales from the
+// The step decodes a block's moments, forms the new ones as the fp32 step does
+// (the operations and roundings of adamw_math.h: codes hang on their last
+// bits), updates the parameter, takes the block's two new scales from the
 // largest magnitudes and stores the codes: 4 bytes of moments per element
 // (read and written) instead of 16.
+//
+// A wave takes one chunk of kQ8Pad = 1024 elements, 4 blocks, 16 elements per
+// lane: what a wave does once (finding its tensor, the clip coefficient in
+// binary64, one access for all its codes) is then spread over 16 elements.
 #include "adamw_math.h"
 #include "q8.h"
 
@@ -12,11 +17,39 @@ namespace zs {
 namespace {
 
 constexpr int kWave = 64;
+constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per wave
+#ifndef STEP_LDS
+#define STEP_LDS 0
+#endif
+#ifndef CODEC_LDS
+#define CODEC_LDS 0
+#endif
+constexpr unsigned kStepLds = STEP_LDS;
+constexpr unsigned kCodecLds = CODEC_LDS;
 
-// Up to 4 consecutive elements from `i` of n (zeros past the end).
+// Where a wave works: its tensor's entry and its chunk.
+struct Chunk {
+    const Q8Entry& e;
+    int64_t first;     // of the entry, of the chunk's elements
+    int64_t i;         // of the lane's first block's elements
+    uint8_t* m;        // the lane's codes
+    uint8_t* v;
+    uint2* scales;     // the chunk's
+};
+__device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
+    uint32_t first_tile;
+    const Q8Entry& e = b.e[find_tensor(b.tab, blockIdx.x, first_tile)];
+    const Q8At at = q8_at(e);
+    const int64_t first = (int64_t)(blockIdx.x - first_tile) * kQ8Pad;
+    return Chunk{e, first, first + threadIdx.x * 4,
+                 at.m + first + threadIdx.x * 16, at.v + first + threadIdx.x * 16,
+                 reinterpret_cast<uint2*>(at.scales + first / (kQ8Block / 2))};
+}
+
+// 4 consecutive elements from i of n (zeros past the end).
 template <typename T>
-__device__ __forceinline__ void load_upto4(const T* p, int64_t i, int64_t n, float (&x)[4]) {
-    if (i + 4 <= n) {
+__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool whole, float (&x)[4]) {
+    if (whole || i + 4 <= n) {
         const f32x4 w = ld4(p + i);
         x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
     } else {
@@ -24,108 +57,190 @@ __device__ __forceinline__ void load_upto4(const T* p, int64_t i, int64_t n, flo
         for (int j = 0; j < 4; ++j) x[j] = i + j < n ? widen(p[i + j]) : 0.0f;
     }
 }
+// fp32 to bf16 by the hardware's conversion, to nearest even (a NaN stays one)
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void st4_hw(float* p, const f32x4& x) { st4(p, x); }
+__device__ __forceinline__ void st4_hw(uint16_t* p, const f32x4& x) {
+    const u32x2 w = __builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4));
+    __builtin_nontemporal_store(u32x2_any(w), reinterpret_cast<u32x2_any*>(p));
+}
 template <typename T>
-__device__ __forceinline__ void store_upto4(T* p, int64_t i, int64_t n, const float (&x)[4]) {
-    if (i + 4 <= n) {
-        st4(p + i, f32x4{x[0], x[1], x[2], x[3]});
+__device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, bool whole, const float (&x)[4]) {
+    if (whole || i + 4 <= n) {
+        st4_hw(p + i, f32x4{x[0], x[1], x[2], x[3]});
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (i + j < n) st1(p + i + j, x[j]);
     }
 }
-// the code word of 4 elements from i (a multiple of 4: inside the padded codes)
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
-    return i < n ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + i)) : 0u;
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[kBlocks]) {
+    const u32x4 x = ld_stream(reinterpret_cast<const u32x4*>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, uint32_t w) {
-    if (i < n) __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(p + i));
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[kBlocks]) {
+    st_stream(reinterpret_cast<u32x4*>(p), u32x4{w[0], w[1], w[2], w[3]});
 }
-// both scale bytes of the block that starts at element i (uniform)
-__device__ __forceinline__ uint16_t* scale_at(const Q8At& at, int64_t i) {
-    return reinterpret_cast<uint16_t*>(at.scales + i / (kQ8Block / 2));
+
+// The chunk's scale bytes as two words: block b's exp_avg byte and exp_avg_sq
+// byte are the bytes 2b and 2b + 1.
+__device__ __forceinline__ uint32_t scale_m(const uint2& s, int b) {
+    return ((b < 2 ? s.x : s.y) >> (16 * (b & 1))) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t scale_v(const uint2& s, int b) {
+    return ((b < 2 ? s.x : s.y) >> (16 * (b & 1) + 8)) & 0xFFu;
+}
+
+// Stores the moments of a chunk: the blocks' scales from their largest
+// magnitudes, then the codes.
+__device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, const float (&m)[kBlocks][4],
+                                              const float (&v)[kBlocks][4]) {
+    uint32_t mc[kBlocks], vc[kBlocks];
+    uint32_t scales[2] = {0, 0};
+    const uint32_t tensor_key = q8_mix(key + c.e.index * kGolden);
+    const uint64_t group = ((uint64_t)c.e.off * kQ8Pad + (uint64_t)c.i) / 4;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        const uint32_t em = q8_scale(wave_max(max4(m[b]))), ev = q8_scale(wave_max(max4(v[b])));
+        const uint32_t word = q8_word(group + b * (kQ8Block / 4), tensor_key);
+        mc[b] = q8_encode4<kTopM>(m[b], em, word);
+        vc[b] = q8_encode4<kTopV>(v[b], ev, word);
+        scales[b / 2] |= (em | ev << 8) << (16 * (b & 1));
+    }
+    store_codes(c.m, mc);
+    store_codes(c.v, vc);
+    if (threadIdx.x == 0) *c.scales = uint2{scales[0], scales[1]};
+}
+
+// the step u of one element from its new moments
+template <bool FAST>
+__device__ __forceinline__ float adam_u(const AdamwScalars& a, float inv_root, float m, float v) {
+    if constexpr (FAST) {
+        // The hardware's square root and reciprocal are within 1 ulp: u is
+        // within 8 * 2^-24 of the exact quotient, far below the parameter's
+        // own rounding, for 11 issue slots against about 50 for IEEE division
+        // and root.  They flush subnormals: den is at least eps, and a
+        // subnormal v's root is below 2^-63.
+        const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), inv_root, a.eps);
+        return m * __builtin_amdgcn_rcpf(den) * a.step_size;
+    }
+    float den = sqrtf(v) / a.bias_correction2_sqrt;
+    den = den + a.eps;
+    return m / den * a.step_size;
+}
+constexpr float kFastEps = 0x1p-40f;
+
+// One chunk's step.  WHOLE: all its elements are the tensor's.
+template <bool PBF16, bool GBF16, bool WHOLE, bool FAST>
+__device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc, const Chunk& c) {
+    using P = typename GradType<PBF16>::T;
+    using G = typename GradType<GBF16>::T;
+    const int64_t n = c.e.numel;
+    P* const param = static_cast<P*>(c.e.param);
+    const G* const grad = static_cast<const G*>(c.e.grad);
+    float g[kBlocks][4], p[kBlocks][4], m[kBlocks][4], v[kBlocks][4];
+    uint32_t mc[kBlocks], vc[kBlocks];
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) load4(grad, c.i + k * kQ8Block, n, WHOLE, g[k]);
+    load_codes(c.m, mc);
+    load_codes(c.v, vc);
+    uint2 scales = *c.scales;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) load4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
+    float coef;
+    if (!clip_coef(sc.adamw, b.norm_sq, coef)) return;
+    scales.x = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.x);
+    scales.y = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.y);
+    const AdamwScalars& a = sc.adamw;
+    const float inv_root = 1.0f / a.bias_correction2_sqrt;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const uint32_t em = scale_m(scales, k), ev = scale_v(scales, k);
+        // beta * value: the scale, a power of two, goes into the factor, which
+        // changes no bit of the product
+        float keep_m = a.beta1, keep_v = a.beta2;
+        if (plain_scale<kTopM>(em) && plain_scale<kTopV>(ev)) {
+            q8_unpack4<kTopM>(mc[k], m[k]);
+            q8_unpack4<kTopV>(vc[k], v[k]);
+            keep_m *= exp2_of((int)em - kTopM);
+            keep_v *= exp2_of((int)ev - kTopV);
+        } else {
+            q8_decode4<kTopM>(mc[k], em, m[k]);
+            q8_decode4<kTopV>(vc[k], ev, v[k]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float gj = g[k][j] * a.grad_scale;
+            gj = gj * coef;
+            const float m_keep = keep_m * m[k][j], m_new = a.one_minus_beta1 * gj;
+            m[k][j] = m_keep + m_new;
+            const float v_keep = keep_v * v[k][j], v_new = a.one_minus_beta2 * (gj * gj);
+            v[k][j] = v_keep + v_new;
+            p[k][j] = apply_step(a, p[k][j], adam_u<FAST>(a, inv_root, m[k][j], v[k][j]));
+            // past the end: no part of the block's scale
+            if (!WHOLE && c.i + k * kQ8Block + j >= n) m[k][j] = v[k][j] = 0.0f;
+        }
+        store4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
+        if (!PBF16 && c.e.copy != nullptr)
+            store4(static_cast<uint16_t*>(c.e.copy), c.i + k * kQ8Block, n, WHOLE, p[k]);
+    }
+    store_moments(c, sc.key, m, v);
 }
 
 template <bool PBF16, bool GBF16, bool DEV>
 __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
-    using P = typename GradType<PBF16>::T;
-    using G = typename GradType<GBF16>::T;
-    uint32_t first;
-    const int t = find_tensor(b.tab, blockIdx.x, first);
-    const Q8Entry& e = b.e[t];
+    const Chunk c = chunk_of(b);
     const Q8Scalars sc = DEV ? *b.sc_dev : b.sc;
-    const Q8At at = q8_at(e);
-    const int64_t n = e.numel;
-    const int64_t block = (int64_t)(blockIdx.x - first) * kQ8Block;
-    const int64_t i = block + threadIdx.x * 4;
-    float g[4], p[4], m[4], v[4];
-    load_upto4(static_cast<const G*>(e.grad), i, n, g);
-    load_upto4(static_cast<const P*>(e.param), i, n, p);
-    const uint32_t mc = load_codes(at.m, i, n), vc = load_codes(at.v, i, n);
-    const uint32_t scales = (uint32_t)__builtin_amdgcn_readfirstlane(*scale_at(at, block));
-    float coef;
-    if (!clip_coef(sc.adamw, b.norm_sq, coef)) return;
-    q8_decode4<kTopM>(mc, scales & 0xFFu, m);
-    q8_decode4<kTopV>(vc, scales >> 8, v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float u = adam_elem(sc.adamw, coef, g[j], m[j], v[j]);
-        p[j] = apply_step(sc.adamw, p[j], u);
-        if (i + j >= n) m[j] = v[j] = 0.0f;   // past the end: no part of the block's scale
-    }
-    store_upto4(static_cast<P*>(e.param), i, n, p);
-    if (!PBF16 && e.copy != nullptr) store_upto4(static_cast<uint16_t*>(e.copy), i, n, p);
-    const uint32_t em = q8_scale(wave_max(max4(m))), ev = q8_scale(wave_max(max4(v)));
-    const uint64_t group = ((uint64_t)e.off * kQ8Pad + (uint64_t)i) / 4;
-    const uint32_t word = q8_word(group, q8_mix(sc.key + e.index * kGolden));
-    store_codes(at.m, i, n, q8_encode4<kTopM>(m, em, word));
-    store_codes(at.v, i, n, q8_encode4<kTopV>(v, ev, word));
-    if (threadIdx.x == 0) *scale_at(at, block) = (uint16_t)(em | ev << 8);
+    if (c.first + kQ8Pad <= (int64_t)c.e.numel && sc.adamw.eps >= kFastEps) step_chunk<PBF16, GBF16, true, true>(b, sc, c);
+    else step_chunk<PBF16, GBF16, false, false>(b, sc, c);
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
-    uint32_t first;
-    const int t = find_tensor(b.tab, blockIdx.x, first);
-    const Q8Entry& e = b.e[t];
-    const Q8At at = q8_at(e);
-    const int64_t n = e.numel;
-    const int64_t block = (int64_t)(blockIdx.x - first) * kQ8Block;
-    const int64_t i = block + threadIdx.x * 4;
-    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (e.param != nullptr) load_upto4(static_cast<const T*>(e.param), i, n, m);
-    if (e.grad != nullptr) load_upto4(static_cast<const T*>(e.grad), i, n, v);
+    const Chunk c = chunk_of(b);
+    const int64_t n = c.e.numel;
+    const bool whole = c.first + kQ8Pad <= n;
+    float m[kBlocks][4] = {}, v[kBlocks][4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(magnitude(v[j]));
-    const uint32_t em = q8_scale(wave_max(max4(m))), ev = q8_scale(wave_max(max4(v)));
-    const uint64_t group = ((uint64_t)e.off * kQ8Pad + (uint64_t)i) / 4;
-    const uint32_t word = q8_word(group, q8_mix(b.sc.key + e.index * kGolden));
-    store_codes(at.m, i, n, q8_encode4<kTopM>(m, em, word));
-    store_codes(at.v, i, n, q8_encode4<kTopV>(v, ev, word));
-    if (threadIdx.x == 0) *scale_at(at, block) = (uint16_t)(em | ev << 8);
+    for (int k = 0; k < kBlocks; ++k) {
+        const int64_t i = c.i + k * kQ8Block;
+        if (c.e.param != nullptr) load4(static_cast<const T*>(c.e.param), i, n, whole, m[k]);
+        if (c.e.grad != nullptr) load4(static_cast<const T*>(c.e.grad), i, n, whole, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[k][j] = __uint_as_float(magnitude(v[k][j]));
+    store_moments(c, b.sc.key, m, v);
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
-    uint32_t first;
-    const int t = find_tensor(b.tab, blockIdx.x, first);
-    const Q8Entry& e = b.e[t];
-    const Q8At at = q8_at(e);
-    const int64_t n = e.numel;
-    const int64_t block = (int64_t)(blockIdx.x - first) * kQ8Block;
-    const int64_t i = block + threadIdx.x * 4;
-    const uint32_t mc = load_codes(at.m, i, n), vc = load_codes(at.v, i, n);
-    const uint32_t scales = (uint32_t)__builtin_amdgcn_readfirstlane(*scale_at(at, block));
-    float x[4];
-    if (e.param != nullptr) {
-        q8_decode4<kTopM>(mc, scales & 0xFFu, x);
-        store_upto4(static_cast<T*>(e.param), i, n, x);
-    }
-    if (e.copy != nullptr) {
-        q8_decode4<kTopV>(vc, scales >> 8, x);
-        store_upto4(static_cast<T*>(e.copy), i, n, x);
+    const Chunk c = chunk_of(b);
+    const int64_t n = c.e.numel;
+    const bool whole = c.first + kQ8Pad <= n;
+    uint32_t mc[kBlocks], vc[kBlocks];
+    load_codes(c.m, mc);
+    load_codes(c.v, vc);
+    uint2 scales = *c.scales;
+    scales.x = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.x);
+    scales.y = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.y);
+    T* const m = static_cast<T*>(c.e.param);
+    T* const v = static_cast<T*>(c.e.copy);
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const int64_t i = c.i + k * kQ8Block;
+        float x[4];
+        if (m != nullptr) {
+            q8_decode4<kTopM>(mc[k], scale_m(scales, k), x);
+            store4(m, i, n, whole, x);
+        }
+        if (v != nullptr) {
+            q8_decode4<kTopV>(vc[k], scale_v(scales, k), x);
+            store4(v, i, n, whole, x);
+        }
     }
 }
 
@@ -133,16 +248,13 @@ template <bool PBF16, bool GBF16>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, 0, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, kStepLds, stream, b);
     else
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, 0, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, kStepLds, stream, b);
     return hipGetLastError();
 }
 
 }  // namespace
-
-int64_t q8_step_tile() { return kQ8Block; }
-int64_t q8_codec_tile() { return kQ8Block; }
 
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream) {
     if (param_bf16)
@@ -152,15 +264,15 @@ hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int6
 
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, 0, stream, b);
-    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, 0, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, kCodecLds, stream, b);
+    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, kCodecLds, stream, b);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, 0, stream, b);
-    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, 0, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, kCodecLds, stream, b);
+    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, kCodecLds, stream, b);
     return hipGetLastError();
 }
 

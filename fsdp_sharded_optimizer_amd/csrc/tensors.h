@@ -121,7 +121,8 @@ hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf
 // --- 8-bit moments --------------------------------------------------------
 // Layout of one tensor's buffer of n elements, P = n rounded up to
 // kQ8Pad: P exp_avg codes, P exp_avg_sq codes, then two bytes per block
-// (exp_avg's e, exp_avg_sq's e).
+// (exp_avg's e, exp_avg_sq's e); the order of the codes is in q8.h.  A
+// workgroup takes kQ8Pad elements.
 constexpr int64_t kQ8Block = 256;
 constexpr int64_t kQ8Pad = 1024;
 __host__ __device__ __forceinline__ int64_t q8_padded(int64_t n) { return (n + kQ8Pad - 1) / kQ8Pad * kQ8Pad; }
@@ -154,8 +155,6 @@ struct Q8Batch {
     Q8Entry e[kListMax];
 };
 static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
-int64_t q8_step_tile();          // elements per workgroup of the step
-int64_t q8_codec_tile();         // and of the conversions
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);

@@ -93,7 +93,7 @@ ZS_API int32_t adamw_step_tensors_dev(const zs_adamw_scalars* scalars_dev, const
  * A code is a small binary floating-point number with 3 fraction bits:
  * exp_avg a sign and 4 exponent bits, exp_avg_sq 5 exponent bits.  With M the
  * block's largest magnitude as a binary32 bit pattern,
- *   e = (M + 0x0FFFFF) >> 23        (one byte per block and moment)
+ *   e = min(255, (M + 0x0FFFFF) >> 23)   (one byte per block and moment)
  *   s = |x| * 2^(T - e), T = 15 (exp_avg) or 31 (exp_avg_sq), in binary32
  *   code = (pattern(s) + r) >> 20   (exp_avg: the sign of x above it;
  *                                    exp_avg_sq: at least 1 for x > 0)

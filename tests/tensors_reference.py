@@ -42,7 +42,7 @@ def encode(x, name, word):
     blocks = -(-n // BLOCK)
     most = np.zeros(blocks * BLOCK, np.int64)
     most[:n] = size
-    e = (most.reshape(blocks, BLOCK).max(axis=1) + 0x0FFFFF) >> 23
+    e = np.minimum((most.reshape(blocks, BLOCK).max(axis=1) + 0x0FFFFF) >> 23, 255)
     k = top - np.repeat(e, BLOCK)[:n]
     with np.errstate(all="ignore"):
         s = np.ldexp(size.astype(np.uint32).view(np.float32).astype(np.float64), k).astype(np.float32)

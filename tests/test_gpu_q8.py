@@ -86,7 +86,7 @@ def test_conversion_edges():
     f = np.float32
     rows = [np.zeros(300, f), np.full(300, -0.0, f), np.full(256, 1e-44, f), np.full(10, 1.875, f),
             np.full(300, np.nextafter(f(1.875), f(2)), f), np.full(256, 3.1e38, f), np.full(256, 3.3e38, f)]
-    for bad in (np.inf, -np.inf, np.nan):
+    for bad in (np.inf, -np.inf, np.nan, np.uint32(0x7FFFFFFF).view(f), np.uint32(0xFFFFFFFF).view(f)):
         x = np.ones(600, f)
         x[299] = bad
         rows.append(x)
