@@ -18,35 +18,42 @@ __host__ __device__ __forceinline__ uint32_t q8_mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// the dither word of the first of 4 consecutive elements (the group G = i / 4
-// of its tensor); the j-th's is j * kGolden more
-__device__ __forceinline__ uint32_t q8_word(uint64_t group, uint32_t tensor_key) {
-    return q8_mix((uint32_t)group + (uint32_t)(group >> 32) * kGolden + tensor_key);
+// the dither word of the first element of the group G = i / 4 of a tensor,
+// before its mixing (the mixed word's j-th element's is j * kGolden more)
+__device__ __forceinline__ uint32_t q8_group(uint64_t group, uint32_t tensor_key) {
+    return (uint32_t)group + (uint32_t)(group >> 32) * kGolden + tensor_key;
 }
 
-// Largest of the 64 lanes' values, in every lane.  DPP within the wave: shifts
-// inside the 16-lane rows, then the two broadcasts across them; lane 63 has
-// the result.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
-    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
-    return x > y ? x : y;
+// The largest of the 64 lanes' values, for 8 values at once: x[k]'s result ends
+// in lane max8_lane(k).  Each step halves the registers while it reduces: after
+// exchanging the halves (rows) of two registers, one maximum reduces both.  22
+// operations for the eight, against 6 each for a reduction of its own.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {   // lanes 0-31: a, 32-63: b
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return max2(r[0], r[1]);
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-    x = dpp_max<0x111, 0xF>(x);   // row_shr:1
-    x = dpp_max<0x112, 0xF>(x);
-    x = dpp_max<0x114, 0xF>(x);
-    x = dpp_max<0x118, 0xF>(x);
-    x = dpp_max<0x142, 0xA>(x);   // row_bcast:15
-    x = dpp_max<0x143, 0xC>(x);   // row_bcast:31
-    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+__device__ __forceinline__ uint32_t max_rows(uint32_t a, uint32_t b) {     // rows 0, 2: a, rows 1, 3: b
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    return max2(r[0], r[1]);
 }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {   // CTRL: a permutation of the lanes
+    return max2(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max8(const uint32_t (&x)[8]) {
+    const uint32_t lo = dpp_max<0x128>(max_rows(max_halves(x[0], x[1]), max_halves(x[2], x[3])));   // row_ror:8
+    const uint32_t hi = dpp_max<0x128>(max_rows(max_halves(x[4], x[5]), max_halves(x[6], x[7])));
+    uint32_t y = (threadIdx.x & 8) ? hi : lo;
+    y = dpp_max<0xB1>(y);      // quad_perm 1,0,3,2
+    y = dpp_max<0x4E>(y);      // quad_perm 2,3,0,1
+    return dpp_max<0x141>(y);  // row_half_mirror
+}
+__device__ constexpr int max8_lane(int k) { return (k & 1) * 32 + (k & 2) * 8 + (k & 4) * 2; }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t max4(const float (&x)[4]) {
-    const uint32_t a = magnitude(x[0]), b = magnitude(x[1]), c = magnitude(x[2]), d = magnitude(x[3]);
-    const uint32_t p = a > b ? a : b, q = c > d ? c : d;
-    return p > q ? p : q;
+    return max2(max2(magnitude(x[0]), magnitude(x[1])), max2(magnitude(x[2]), magnitude(x[3])));
 }
 // a block's scale byte from its largest magnitude's pattern (NaN patterns are
 // above infinity's, so a non-finite block gets 255)
@@ -67,13 +74,13 @@ __device__ __forceinline__ bool plain_scale(uint32_t e) { return e >= (uint32_t)
 // The 4 codes of a word as binary32 numbers below their scale: value * 2^(TOP - e).
 template <int TOP>
 __device__ __forceinline__ void q8_unpack4(uint32_t codes, float (&x)[4]) {
-    constexpr uint32_t kMask = TOP == kTopM ? 0x87F00000u : 0x0FF00000u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         // exp_avg: the code's sign, extended, ends in bit 31; its 7 other bits in 26..20
-        const uint32_t at20 = TOP == kTopM ? (uint32_t)((int32_t)(codes << (24 - 8 * j)) >> 4)
-                                           : (j < 3 ? codes << (20 - 8 * j) : codes >> 4);
-        x[j] = __uint_as_float(at20 & kMask);
+        if constexpr (TOP == kTopM)
+            x[j] = __uint_as_float(((uint32_t)(int32_t)(int8_t)(codes >> (8 * j)) << 20) & 0x87F00000u);
+        else
+            x[j] = __uint_as_float(((codes >> (8 * j)) & 0xFFu) << 20);
     }
 }
 
@@ -85,27 +92,31 @@ __device__ __forceinline__ void q8_decode4(uint32_t codes, uint32_t e, float (&x
     for (int j = 0; j < 4; ++j) x[j] = e == 255u ? __builtin_nanf("") : __builtin_ldexpf(x[j], (int)e - TOP);
 }
 
+// the top bytes of four words, the first one's lowest
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0703u);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x07030C0Cu), lo, 0x07060100u);
+}
+
 // 4 values into codes; word: the dither word of the first.  The sum cannot
 // carry past the top code: the block's largest magnitude is at most 1.875 times
 // the top exponent's power of two, which is the top code.  (In a block with
 // e = 255 nothing of a code is meaningful; it is only kept inside its byte.)
 template <int TOP>
 __device__ __forceinline__ uint32_t q8_encode4(const float (&x)[4], uint32_t e, uint32_t word) {
-    uint32_t c[4];   // the code in the top byte
+    uint32_t c[4];   // the code (exp_avg: without its sign) in the top byte
     if (plain_scale<TOP>(e)) {
         const float scale = exp2_of(TOP - (int)e);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(x[j] * scale);
+        for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(__builtin_fabsf(x[j]) * scale);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(__builtin_ldexpf(x[j], TOP - (int)e));
+        for (int j = 0; j < 4; ++j) c[j] = magnitude(__builtin_ldexpf(x[j], TOP - (int)e));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t h = word + (uint32_t)j * kGolden;
-        const uint32_t sum = c[j] + (TOP == kTopM ? h >> 12 : h & 0xFFFFFu);
-        if constexpr (TOP == kTopM) c[j] = ((sum << 4) & 0x7FFFFFFFu) | (sum & 0x80000000u);
-        else c[j] = sum << 4;
+        c[j] = (c[j] + (TOP == kTopM ? h >> 12 : h & 0xFFFFFu)) << 4;
     }
     if constexpr (TOP == kTopV) {
         // a positive second moment never becomes 0 (few do: one test for the four)
@@ -116,8 +127,11 @@ __device__ __forceinline__ uint32_t q8_encode4(const float (&x)[4], uint32_t e, 
                 if (c[j] < 0x01000000u && x[j] > 0.0f) c[j] = 0x01000000u;
         }
     }
-    const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0703u);   // top bytes of c[0], c[1]
-    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x07030C0Cu), lo, 0x07060100u);
+    const uint32_t out = top_bytes(c[0], c[1], c[2], c[3]);
+    if constexpr (TOP == kTopV) return out;
+    const uint32_t signs = top_bytes(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                     __float_as_uint(x[3]));
+    return (signs & 0x80808080u) | (out & 0x7F7F7F7Fu);
 }
 
 // Where a tensor's (entry's) codes and scales are.  Codes lie in chunks of

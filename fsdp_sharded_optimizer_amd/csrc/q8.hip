@@ -95,14 +95,21 @@ __device__ __forceinline__ uint32_t scale_v(const uint2& s, int b) {
 // magnitudes, then the codes.
 __device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, const float (&m)[kBlocks][4],
                                               const float (&v)[kBlocks][4]) {
+    static_assert(kBlocks == 4, "8 maxima");
+    uint32_t most[2 * kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) most[2 * b] = max4(m[b]), most[2 * b + 1] = max4(v[b]);
+    const uint32_t e = q8_scale(wave_max8(most));
     uint32_t mc[kBlocks], vc[kBlocks];
     uint32_t scales[2] = {0, 0};
     const uint32_t tensor_key = q8_mix(key + c.e.index * kGolden);
-    const uint64_t group = ((uint64_t)c.e.off * kQ8Pad + (uint64_t)c.i) / 4;
+    // the chunk's first group; its 256 groups share the upper 32 bits
+    const uint32_t group = q8_group(((uint64_t)c.e.off * kQ8Pad + (uint64_t)c.first) / 4, tensor_key);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-        const uint32_t em = q8_scale(wave_max(max4(m[b]))), ev = q8_scale(wave_max(max4(v[b])));
-        const uint32_t word = q8_word(group + b * (kQ8Block / 4), tensor_key);
+        const uint32_t em = (uint32_t)__builtin_amdgcn_readlane((int)e, max8_lane(2 * b));
+        const uint32_t ev = (uint32_t)__builtin_amdgcn_readlane((int)e, max8_lane(2 * b + 1));
+        const uint32_t word = q8_mix(group + b * (uint32_t)(kQ8Block / 4) + threadIdx.x);
         mc[b] = q8_encode4<kTopM>(m[b], em, word);
         vc[b] = q8_encode4<kTopV>(v[b], ev, word);
         scales[b / 2] |= (em | ev << 8) << (16 * (b & 1));
@@ -112,9 +119,9 @@ __device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, cons
     if (threadIdx.x == 0) *c.scales = uint2{scales[0], scales[1]};
 }
 
-// the step u of one element from its new moments
+// u / step_size of one element from its new moments
 template <bool FAST>
-__device__ __forceinline__ float adam_u(const AdamwScalars& a, float inv_root, float m, float v) {
+__device__ __forceinline__ float adam_ratio(const AdamwScalars& a, float inv_root, float m, float v) {
     if constexpr (FAST) {
         // The hardware's square root and reciprocal are within 1 ulp: u is
         // within 8 * 2^-24 of the exact quotient, far below the parameter's
@@ -122,11 +129,11 @@ __device__ __forceinline__ float adam_u(const AdamwScalars& a, float inv_root, f
         // and root.  They flush subnormals: den is at least eps, and a
         // subnormal v's root is below 2^-63.
         const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), inv_root, a.eps);
-        return m * __builtin_amdgcn_rcpf(den) * a.step_size;
+        return m * __builtin_amdgcn_rcpf(den);
     }
     float den = sqrtf(v) / a.bias_correction2_sqrt;
     den = den + a.eps;
-    return m / den * a.step_size;
+    return m / den;
 }
 constexpr float kFastEps = 0x1p-40f;
 
@@ -169,14 +176,19 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
             q8_decode4<kTopV>(vc[k], ev, v[k]);
         }
 #pragma unroll
+        for (int j = 0; j < 4; ++j) g[k][j] = g[k][j] * a.grad_scale;
+        if (coef != 1.0f) {   // (x * 1 is x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[k][j] = g[k][j] * coef;
+        }
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float gj = g[k][j] * a.grad_scale;
-            gj = gj * coef;
+            const float gj = g[k][j];
             const float m_keep = keep_m * m[k][j], m_new = a.one_minus_beta1 * gj;
             m[k][j] = m_keep + m_new;
             const float v_keep = keep_v * v[k][j], v_new = a.one_minus_beta2 * (gj * gj);
             v[k][j] = v_keep + v_new;
-            p[k][j] = apply_step(a, p[k][j], adam_u<FAST>(a, inv_root, m[k][j], v[k][j]));
+            p[k][j] = __builtin_fmaf(-adam_ratio<FAST>(a, inv_root, m[k][j], v[k][j]), a.step_size, p[k][j] * a.decay);
             // past the end: no part of the block's scale
             if (!WHOLE && c.i + k * kQ8Block + j >= n) m[k][j] = v[k][j] = 0.0f;
         }
