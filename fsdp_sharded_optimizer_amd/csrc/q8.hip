@@ -18,14 +18,19 @@ namespace {
 
 constexpr int kWave = 64;
 constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per wave
-#ifndef STEP_LDS
-#define STEP_LDS 0
-#endif
-#ifndef CODEC_LDS
-#define CODEC_LDS 0
-#endif
-constexpr unsigned kStepLds = STEP_LDS;
-constexpr unsigned kCodecLds = CODEC_LDS;
+// LDS reserved (never touched) per workgroup to cap how many share a CU: too
+// many keep too many DRAM rows open.  Measured on 809M fp32 parameters with bf16
+// gradients and re-casts (855M bf16 parameters; 317M moments to and from bf16),
+// of the 8 TB/s peak: step 73.1 % at 6 KiB, 75.5 at 8, 76.4 at 10, 77.3 at 12,
+// 77.6 at 14, 76.4 at 16 (bf16: 78.7 at 6, 79.6 at 8, 79.8 at 10, 78.6 at 12, 74.7 at
+// 14: fewer bytes per wave want more waves); read-out 75.9 % uncapped, 78.9 at
+// 8 KiB, 68.2 at 12; storing 68.1 % uncapped, 70.3 at 4 KiB, 60.4 at 6.  Two blocks
+// per wave instead of four: the step within 0.3 points at its best cap, storing
+// 4 points slower; 2 or 4 waves per workgroup: 0.5-4 points slower; plain instead
+// of streaming code accesses: the step 1 point slower.
+template <bool PBF16> constexpr unsigned kStepLds = PBF16 ? 10240 : 14336;
+constexpr unsigned kEncodeLds = 4096;
+constexpr unsigned kDecodeLds = 8192;
 
 // Where a wave works: its tensor's entry and its chunk.
 struct Chunk {
@@ -42,7 +47,7 @@ __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
     const Q8At at = q8_at(e);
     const int64_t first = (int64_t)(blockIdx.x - first_tile) * kQ8Pad;
     return Chunk{e, first, first + threadIdx.x * 4,
-                 at.m + first + threadIdx.x * 16, at.v + first + threadIdx.x * 16,
+                 at.codes + 2 * first + threadIdx.x * 16, at.codes + 2 * first + kQ8Pad + threadIdx.x * 16,
                  reinterpret_cast<uint2*>(at.scales + first / (kQ8Block / 2))};
 }
 
@@ -260,9 +265,9 @@ template <bool PBF16, bool GBF16>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, kStepLds, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, kStepLds<PBF16>, stream, b);
     else
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, kStepLds, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, kStepLds<PBF16>, stream, b);
     return hipGetLastError();
 }
 
@@ -276,15 +281,15 @@ hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int6
 
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, kCodecLds, stream, b);
-    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, kCodecLds, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, kEncodeLds, stream, b);
+    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, kEncodeLds, stream, b);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, kCodecLds, stream, b);
-    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, kCodecLds, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, kDecodeLds, stream, b);
+    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, kDecodeLds, stream, b);
     return hipGetLastError();
 }
 

@@ -119,10 +119,9 @@ hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf
                                 hipStream_t stream);
 
 // --- 8-bit moments --------------------------------------------------------
-// Layout of one tensor's buffer of n elements, P = n rounded up to
-// kQ8Pad: P exp_avg codes, P exp_avg_sq codes, then two bytes per block
-// (exp_avg's e, exp_avg_sq's e); the order of the codes is in q8.h.  A
-// workgroup takes kQ8Pad elements.
+// Layout of one tensor's buffer of n elements, P = n rounded up to kQ8Pad:
+// 2 P bytes of codes (their order is in q8.h), then two bytes per block (exp_avg's
+// e, exp_avg_sq's e).  A workgroup takes kQ8Pad elements.
 constexpr int64_t kQ8Block = 256;
 constexpr int64_t kQ8Pad = 1024;
 __host__ __device__ __forceinline__ int64_t q8_padded(int64_t n) { return (n + kQ8Pad - 1) / kQ8Pad * kQ8Pad; }
