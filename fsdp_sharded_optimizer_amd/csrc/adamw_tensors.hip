@@ -2,7 +2,7 @@
 //
 // The update of one element is adamw.hip's (adamw_math.h: the same operations
 // and roundings, so a tensor gets the bits adamw_step or adamw_step_no_master
-// would give it); here one launch covers up to 64 tensors of any sizes.
+// would give it); here one launch covers up to 98 tensors of any sizes.
 // HBM-bound: with fp32 parameters 24 B/element of parameter and moments plus
 // the gradient (2 or 4) and the bf16 re-cast (2); with bf16 parameters 20 plus
 // the gradient.
@@ -17,27 +17,40 @@ namespace zs {
 namespace {
 
 constexpr int kWave = 64;
-constexpr unsigned kLds = 16384;
+// LDS reserved (never touched) per workgroup, to cap how many share a CU (too
+// many keep too many DRAM rows open): the cap that keeps about 80 KiB in flight
+// per CU.  Measured, % of the 8 TB/s peak at 8 / 10 / 12 / 13 / 14 / 16 KiB:
+// fp32 parameters with re-casts, fp32 gradients (634M) 77.1 / 77.1 / 79.1 / 80.6 /
+// 82.6 / 81.1, bf16 gradients (809M) 78.9 / 79.3 / 82.1 / 82.8 / 81.8 / 78.8; bf16
+// parameters, fp32 gradients (134M) 77 / 78 / 82 / 82 / 79, bf16 gradients (855M)
+// 81 / 82 / 81 / 78 / 74; uncapped 74-79.  A launch of less than 8M elements is
+// not long enough for that and ends sooner with more of it resident: 290
+// tensors of 25M bf16 parameters in five launches 107 us uncapped, 115 at 12 KiB.
+template <bool PBF16, bool GBF16>
+constexpr unsigned kLds = PBF16 ? (GBF16 ? 10240 : 12288) : (GBF16 ? 13312 : 14336);
+constexpr int64_t kCapTiles = 32768;
 
 template <bool PBF16, bool GBF16, bool DEV>
 __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b) {
     using P = typename GradType<PBF16>::T;
     using G = typename GradType<GBF16>::T;
     uint32_t first;
-    const int t = find_tensor(b.tab, blockIdx.x, first);
-    const AdamwEntry& e = b.e[t];
+    const AdamwEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
     const AdamwScalars sc = DEV ? *b.sc_dev : b.sc;
-    P* const param = static_cast<P*>(e.param);
-    const G* const grad = static_cast<const G*>(e.grad);
+    P* const param = unpack_ptr<P>(e.lo[0], e.hi[0]);
+    const G* const grad = unpack_ptr<const G>(e.lo[1], e.hi[0] >> 16);
+    float* const exp_avg = unpack_ptr<float>(e.lo[2], e.hi[1]);
+    float* const exp_avg_sq = unpack_ptr<float>(e.lo[3], e.hi[1] >> 16);
+    uint16_t* const copy = unpack_ptr<uint16_t>(e.lo[4], e.hi[2]);
     const int64_t n = e.numel;
-    const int64_t i = (int64_t)(blockIdx.x - first) * kListTile - e.shift + threadIdx.x * 4;
+    const int64_t i = (int64_t)(blockIdx.x - first) * kListTile - (e.hi[2] >> 16) + threadIdx.x * 4;
     float coef;
     if (i >= 0 && i + 4 <= n) {
         // the loads are issued before the clip coefficient is resolved
         const f32x4 g4 = ld4(grad + i);
         f32x4 p4 = ld4(param + i);
-        f32x4 m4 = ld4(e.exp_avg + i);
-        f32x4 v4 = ld4(e.exp_avg_sq + i);
+        f32x4 m4 = ld4(exp_avg + i);
+        f32x4 v4 = ld4(exp_avg_sq + i);
         if (!clip_coef(sc, b.norm_sq, coef)) return;
         float gs[4] = {g4.x, g4.y, g4.z, g4.w};
         float ps[4] = {p4.x, p4.y, p4.z, p4.w};
@@ -50,9 +63,9 @@ __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b
         }
         const f32x4 po = {ps[0], ps[1], ps[2], ps[3]};
         st4(param + i, po);
-        st4(e.exp_avg + i, f32x4{ms[0], ms[1], ms[2], ms[3]});
-        st4(e.exp_avg_sq + i, f32x4{vs[0], vs[1], vs[2], vs[3]});
-        if (!PBF16 && e.copy != nullptr) st4(e.copy + i, po);
+        st4(exp_avg + i, f32x4{ms[0], ms[1], ms[2], ms[3]});
+        st4(exp_avg_sq + i, f32x4{vs[0], vs[1], vs[2], vs[3]});
+        if (!PBF16 && copy != nullptr) st4(copy + i, po);
         return;
     }
     // lanes across a tensor's start or end (or outside it)
@@ -61,23 +74,24 @@ __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b
     for (int j = 0; j < 4; ++j) {
         const int64_t k = i + j;
         if (k < 0 || k >= n) continue;
-        float m = e.exp_avg[k], v = e.exp_avg_sq[k];
+        float m = exp_avg[k], v = exp_avg_sq[k];
         const float u = adam_elem(sc, coef, widen(grad[k]), m, v);
         const float p = apply_step(sc, widen(param[k]), u);
         st1(param + k, p);
-        e.exp_avg[k] = m;
-        e.exp_avg_sq[k] = v;
-        if (!PBF16 && e.copy != nullptr) st1(e.copy + k, p);
+        exp_avg[k] = m;
+        exp_avg_sq[k] = v;
+        if (!PBF16 && copy != nullptr) st1(copy + k, p);
     }
 }
 
 template <bool PBF16, bool GBF16>
 hipError_t launch(const AdamwBatch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
+    const unsigned lds = tiles < kCapTiles ? 0 : kLds<PBF16, GBF16>;
     if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, true>), grid, block, kLds, stream, b);
+        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, true>), grid, block, lds, stream, b);
     else
-        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, false>), grid, block, kLds, stream, b);
+        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, false>), grid, block, lds, stream, b);
     return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
 // C-ABI entry points over lists of tensors (include/zshard_tensors.h):
-// validation on the host, then launches of up to 64 tensors each.
+// validation on the host, then launches of as many tensors as their tables hold.
 #include <algorithm>
 #include <cstddef>
 #include <cstdlib>
@@ -19,39 +19,82 @@ static_assert(kLaunchElems % kQ8Pad == 0 && kLaunchElems % kListTile == 0, "piec
 namespace {
 
 // The byte ranges of one call, and whether any written one shares a byte with
-// another.  Sorted by address: O(k log k), since a list of some hundred
-// tensors has thousands of buffers (pairwise, milliseconds).
+// another.  Merged in address order: a list of some hundred tensors has
+// thousands of buffers (pairwise: milliseconds).  They come tensor after
+// tensor, one kind of buffer at a time in ascending order for most programs
+// (views of one buffer, an allocator that moves up), so each kind is kept as a
+// sequence of its own, sorted only if it is not in order, and the sequences
+// are walked together.
 struct Range {
     uintptr_t lo, hi;
-    bool written;
 };
 
-struct Ranges {
-    Range* r = nullptr;
-    int64_t count = 0;
-    Range few[512];
-
-    // false: no memory for the table
-    bool reserve(int64_t most) {
-        r = most <= (int64_t)(sizeof(few) / sizeof(few[0])) ? few : static_cast<Range*>(std::malloc(most * sizeof(Range)));
-        return r != nullptr;
+class Ranges {
+public:
+    static constexpr int kKinds = 6;
+    // room for `count` ranges of each kind; false: no memory
+    bool reserve(int32_t count, int kinds) {
+        per_ = (int64_t)count;
+        const int64_t most = per_ * kinds;
+        all_ = most <= kFew ? few_ : static_cast<Range*>(std::malloc((size_t)most * sizeof(Range)));
+        return all_ != nullptr;
     }
+    Ranges() = default;
+    Ranges(const Ranges&) = delete;
+    Ranges& operator=(const Ranges&) = delete;
     ~Ranges() {
-        if (r != few) std::free(r);
+        if (all_ != few_) std::free(all_);
     }
-    void add(const void* p, int64_t bytes, bool written) {
-        if (p != nullptr && bytes > 0) r[count++] = Range{addr(p), addr(p) + (uintptr_t)bytes, written};
+    void add(int kind, const void* p, int64_t bytes, bool written) {
+        if (p == nullptr || bytes <= 0) return;
+        Range* const r = all_ + kind * per_;
+        int64_t& n = count_[kind];
+        written_[kind] = written;
+        r[n] = Range{addr(p), addr(p) + (uintptr_t)bytes};
+        if (n > 0 && r[n].lo < r[n - 1].lo) sorted_[kind] = false;
+        ++n;
+    }
+    // one range more that is read (the norm, the scalars)
+    void add_read(const void* p, int64_t bytes) {
+        if (p != nullptr) extra_[extras_++] = Range{addr(p), addr(p) + (uintptr_t)bytes};
     }
     bool clash() {
-        std::sort(r, r + count, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        int64_t at[kKinds] = {};
+        for (int k = 0; k < kKinds; ++k)
+            if (!sorted_[k])
+                std::sort(all_ + k * per_, all_ + k * per_ + count_[k],
+                          [](const Range& a, const Range& b) { return a.lo < b.lo; });
         uintptr_t written_to = 0, any_to = 0;   // how far the ranges before this one reach
-        for (int64_t i = 0; i < count; ++i) {
-            if (r[i].lo < written_to || (r[i].written && r[i].lo < any_to)) return true;
-            any_to = std::max(any_to, r[i].hi);
-            if (r[i].written) written_to = std::max(written_to, r[i].hi);
+        for (;;) {
+            int next = -1;
+            uintptr_t lo = 0;
+            for (int k = 0; k < kKinds; ++k) {
+                if (at[k] == count_[k]) continue;
+                const uintptr_t x = all_[k * per_ + at[k]].lo;
+                if (next < 0 || x < lo) next = k, lo = x;
+            }
+            if (next < 0) break;
+            const Range& r = all_[next * per_ + at[next]++];
+            if (r.lo < written_to || (written_[next] && r.lo < any_to)) return true;
+            any_to = std::max(any_to, r.hi);
+            if (!written_[next]) continue;
+            written_to = std::max(written_to, r.hi);
+            for (int x = 0; x < extras_; ++x)
+                if (r.lo < extra_[x].hi && extra_[x].lo < r.hi) return true;
         }
         return false;
     }
+
+private:
+    static constexpr int64_t kFew = 512;
+    Range few_[kFew];
+    Range* all_ = few_;
+    int64_t per_ = 0;
+    int64_t count_[kKinds] = {};
+    bool written_[kKinds] = {};
+    bool sorted_[kKinds] = {true, true, true, true, true, true};
+    Range extra_[2];
+    int extras_ = 0;
 };
 
 // The sum of the list's numels, or -1 for a bad list.
@@ -73,7 +116,7 @@ public:
     Filler(Batch& b, Launch launch) : b_(b), launch_(launch) { clear(); }
     // room for an entry of `tiles` workgroups; the entry's place in out
     int32_t add(int64_t tiles, int& out) {
-        if (count_ == kListMax || tiles_ + tiles > kListMaxTiles) {
+        if (count_ == decltype(b_.tab)::kMax || tiles_ + tiles > kListMaxTiles) {
             const int32_t rc = flush();
             if (rc != ZS_OK) return rc;
         }
@@ -135,7 +178,7 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
     }
     const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
     Ranges ranges;
-    if (!ranges.reserve((int64_t)count * 5 + 2)) return ZS_EINVAL;
+    if (!ranges.reserve(count, 5)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_tensor& t = list[k];
         if (t.numel == 0) continue;
@@ -144,14 +187,17 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
             !aligned(t.exp_avg_sq, 4))
             return ZS_EINVAL;
         if (t.param_bf16 != nullptr && (param_dtype == ZS_BF16 || !aligned(t.param_bf16, 2))) return ZS_EINVAL;
-        ranges.add(t.param, t.numel * psz, true);
-        ranges.add(t.grad, t.numel * gsz, false);
-        ranges.add(t.exp_avg, t.numel * 4, true);
-        ranges.add(t.exp_avg_sq, t.numel * 4, true);
-        ranges.add(t.param_bf16, t.numel * 2, true);
+        if (!packable(t.param) || !packable(t.grad) || !packable(t.exp_avg) || !packable(t.exp_avg_sq) ||
+            !packable(t.param_bf16))
+            return ZS_EINVAL;
+        ranges.add(0, t.param, t.numel * psz, true);
+        ranges.add(1, t.grad, t.numel * gsz, false);
+        ranges.add(2, t.exp_avg, t.numel * 4, true);
+        ranges.add(3, t.exp_avg_sq, t.numel * 4, true);
+        ranges.add(4, t.param_bf16, t.numel * 2, true);
     }
-    ranges.add(norm_sq_dev, 8, false);
-    ranges.add(sc_dev, (int64_t)sizeof(zs_adamw_scalars), false);
+    ranges.add_read(norm_sq_dev, 8);
+    ranges.add_read(sc_dev, (int64_t)sizeof(zs_adamw_scalars));
     if (ranges.clash()) return ZS_EOVERLAP;
 
     AdamwBatch b;
@@ -171,14 +217,14 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
             int at = 0;
             const int32_t rc = fill.add(ceil_div(n + shift, kListTile), at);
             if (rc != ZS_OK) return rc;
+            const void* const ptr[5] = {advance(t.param, off * psz), advance(t.grad, off * gsz), t.exp_avg + off,
+                                        t.exp_avg_sq + off, advance(t.param_bf16, off * 2)};
             AdamwEntry& e = b.e[at];
-            e.param = advance(t.param, off * psz);
-            e.grad = advance(t.grad, off * gsz);
-            e.exp_avg = t.exp_avg + off;
-            e.exp_avg_sq = t.exp_avg_sq + off;
-            e.copy = advance(t.param_bf16, off * 2);
+            for (int j = 0; j < 5; ++j) e.lo[j] = ptr_lo(ptr[j]);
+            e.hi[0] = ptr_hi(ptr[0]) | ptr_hi(ptr[1]) << 16;
+            e.hi[1] = ptr_hi(ptr[2]) | ptr_hi(ptr[3]) << 16;
+            e.hi[2] = ptr_hi(ptr[4]) | (uint32_t)shift << 16;
             e.numel = (uint32_t)n;
-            e.shift = (uint32_t)shift;
         }
     }
     return fill.flush();
@@ -186,22 +232,24 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
 
 uint32_t q8_key(uint32_t seed, int64_t step) { return q8_mix(q8_mix(seed) + (uint32_t)step); }
 
-// the entries of one tensor's pieces; `set(entry, element offset)` fills the pointers
-template <typename Fill, typename Set>
-int32_t add_q8(Q8Batch& b, Fill& fill, void* state, int64_t numel, uint32_t index, int64_t tile, Set set) {
+// the entries of one tensor's pieces: `a` and `b` advance by their element
+// sizes, `copy` by 2 bytes
+template <typename Fill>
+int32_t add_q8(Q8Batch& batch, Fill& fill, void* state, int64_t numel, int32_t index, const void* a, int64_t asz,
+               const void* b, int64_t bsz, const void* copy) {
     for (int64_t off = 0; off < numel; off += kLaunchElems) {
         const int64_t n = launch_piece(numel, off);
         int at = 0;
-        const int32_t rc = fill.add(ceil_div(n, tile), at);
+        const int32_t rc = fill.add(ceil_div(n, kQ8Pad), at);
         if (rc != ZS_OK) return rc;
-        Q8Entry& e = b.e[at];
-        std::memset(&e, 0, sizeof(e));
-        e.state = static_cast<uint8_t*>(state);
+        const void* const ptr[4] = {advance(a, off * asz), advance(b, off * bsz), state, advance(copy, off * 2)};
+        Q8Entry& e = batch.e[at];
+        for (int j = 0; j < 4; ++j) e.lo[j] = ptr_lo(ptr[j]);
+        e.hi[0] = ptr_hi(ptr[0]) | ptr_hi(ptr[1]) << 16;
+        e.hi[1] = ptr_hi(ptr[2]) | ptr_hi(ptr[3]) << 16;
         e.numel = (uint32_t)n;
-        e.off = (uint32_t)(off / kQ8Pad);
+        e.index_off = (uint32_t)index | (uint32_t)(off / kLaunchElems) << 24;
         e.padded = (uint32_t)(q8_padded(numel) / kQ8Pad);
-        e.index = index;
-        set(e, off);
     }
     return ZS_OK;
 }
@@ -210,7 +258,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
                         const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                         const double* norm_sq_dev, void* hip_stream) {
     const int64_t total = list_total(list, count);
-    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return ZS_EINVAL;
+    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype) || count > kQ8MaxCount) return ZS_EINVAL;
     if (sc_dev == nullptr) {
         const int32_t rc = adamw_check_hp(hp, total, norm_sq_dev);
         if (rc != ZS_OK) return rc;
@@ -219,7 +267,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
     }
     const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
     Ranges ranges;
-    if (!ranges.reserve((int64_t)count * 4 + 2)) return ZS_EINVAL;
+    if (!ranges.reserve(count, 4)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
         if (t.numel == 0) continue;
@@ -227,13 +275,14 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         if (!aligned(t.param, (uintptr_t)psz) || !aligned(t.grad, (uintptr_t)gsz) || !aligned(t.state_q8, 16))
             return ZS_EINVAL;
         if (t.param_bf16 != nullptr && (param_dtype == ZS_BF16 || !aligned(t.param_bf16, 2))) return ZS_EINVAL;
-        ranges.add(t.param, t.numel * psz, true);
-        ranges.add(t.grad, t.numel * gsz, false);
-        ranges.add(t.state_q8, moments_q8_bytes(t.numel), true);
-        ranges.add(t.param_bf16, t.numel * 2, true);
+        if (!packable(t.param) || !packable(t.grad) || !packable(t.state_q8) || !packable(t.param_bf16)) return ZS_EINVAL;
+        ranges.add(0, t.param, t.numel * psz, true);
+        ranges.add(1, t.grad, t.numel * gsz, false);
+        ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), true);
+        ranges.add(3, t.param_bf16, t.numel * 2, true);
     }
-    ranges.add(norm_sq_dev, 8, false);
-    ranges.add(sc_dev, (int64_t)sizeof(zs_adamw_q8_scalars), false);
+    ranges.add_read(norm_sq_dev, 8);
+    ranges.add_read(sc_dev, (int64_t)sizeof(zs_adamw_q8_scalars));
     if (ranges.clash()) return ZS_EOVERLAP;
 
     Q8Batch b;
@@ -250,11 +299,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, kQ8Pad, [&](Q8Entry& e, int64_t off) {
-            e.param = advance(t.param, off * psz);
-            e.grad = advance(t.grad, off * gsz);
-            e.copy = advance(t.param_bf16, off * 2);
-        });
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.param, psz, t.grad, gsz, t.param_bf16);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();
@@ -263,19 +308,19 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
 // both conversions: encode reads the moments and writes the state, decode the reverse
 int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool encode, uint32_t seed,
                    void* hip_stream) {
-    if (list_total(list, count) < 0 || !dtype_ok(dtype)) return ZS_EINVAL;
+    if (list_total(list, count) < 0 || !dtype_ok(dtype) || count > kQ8MaxCount) return ZS_EINVAL;
     const int64_t sz = elem_size(dtype);
     Ranges ranges;
-    if (!ranges.reserve((int64_t)count * 3)) return ZS_EINVAL;
+    if (!ranges.reserve(count, 3)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
         if (t.numel == 0) continue;
         if (t.state_q8 == nullptr || !aligned(t.state_q8, 16)) return ZS_EINVAL;
-        for (void* p : {t.exp_avg, t.exp_avg_sq}) {
-            if (!aligned(p, (uintptr_t)sz)) return ZS_EINVAL;
-            ranges.add(p, t.numel * sz, !encode);
-        }
-        ranges.add(t.state_q8, moments_q8_bytes(t.numel), encode);
+        if (!aligned(t.exp_avg, (uintptr_t)sz) || !aligned(t.exp_avg_sq, (uintptr_t)sz)) return ZS_EINVAL;
+        if (!packable(t.exp_avg) || !packable(t.exp_avg_sq) || !packable(t.state_q8)) return ZS_EINVAL;
+        ranges.add(0, t.exp_avg, t.numel * sz, !encode);
+        ranges.add(1, t.exp_avg_sq, t.numel * sz, !encode);
+        ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), encode);
     }
     if (ranges.clash()) return ZS_EOVERLAP;
     Q8Batch b;
@@ -289,12 +334,7 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
         if (!encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr) continue;
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, (uint32_t)k, kQ8Pad, [&](Q8Entry& e, int64_t off) {
-            e.param = advance(t.exp_avg, off * sz);
-            void* const v = advance(t.exp_avg_sq, off * sz);
-            if (encode) e.grad = v;
-            else e.copy = v;
-        });
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.exp_avg, sz, t.exp_avg_sq, sz, nullptr);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();
@@ -328,17 +368,16 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
     const int64_t need = grad_norm_sq_tensors_workspace_bytes(grads, count, grad_dtype);
     if (need > 0 && (workspace == nullptr || !aligned(workspace, 8))) return ZS_EINVAL;
     if (workspace_bytes < need) return ZS_EWORKSPACE;
-    Ranges ranges;
-    if (!ranges.reserve((int64_t)count + 2)) return ZS_EINVAL;
+    // only the workspace and *out_sq_dev are written
+    if (overlap(out_sq_dev, 8, workspace, need)) return ZS_EOVERLAP;
+    bool clash = false;
     for (int32_t k = 0; k < count; ++k) {
         const zs_tensor& t = grads[k];
         if (t.numel == 0) continue;
-        if (t.ptr == nullptr || !aligned(t.ptr, (uintptr_t)gsz)) return ZS_EINVAL;
-        ranges.add(t.ptr, t.numel * gsz, false);
+        if (t.ptr == nullptr || !aligned(t.ptr, (uintptr_t)gsz) || !packable(t.ptr)) return ZS_EINVAL;
+        clash = clash || overlap(t.ptr, t.numel * gsz, out_sq_dev, 8) || overlap(t.ptr, t.numel * gsz, workspace, need);
     }
-    ranges.add(out_sq_dev, 8, true);
-    ranges.add(workspace, need, true);
-    if (ranges.clash()) return ZS_EOVERLAP;
+    if (clash) return ZS_EOVERLAP;
 
     double* const partials = static_cast<double*>(workspace);
     int64_t done = 0;   // partials of the launches before
@@ -358,8 +397,8 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
             int at = 0;
             const int32_t rc = fill.add(ceil_div(n, tile), at);
             if (rc != ZS_OK) return rc;
-            b.e[at].grad = advance(grads[k].ptr, off * gsz);
-            b.e[at].numel = n;
+            const void* const p = advance(grads[k].ptr, off * gsz);
+            b.e[at] = NormEntry{ptr_lo(p), ptr_hi(p), (uint32_t)n};
         }
     const int32_t rc = fill.flush();
     if (rc != ZS_OK) return rc;

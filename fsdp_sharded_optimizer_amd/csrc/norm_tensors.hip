@@ -29,9 +29,9 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     constexpr int VE = kVec<BF16>;
     using T = typename GradType<BF16>::T;
     uint32_t first;
-    const int t = find_tensor(b.tab, blockIdx.x, first);
-    const T* const grad = static_cast<const T*>(b.e[t].grad);
-    const int64_t n = b.e[t].numel;
+    const NormEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
+    const T* const grad = unpack_ptr<const T>(e.lo, e.hi);
+    const int64_t n = e.numel;
     const int64_t tile = (int64_t)(blockIdx.x - first) * kTile<BF16>;
     const int64_t lane0 = tile + threadIdx.x * VE;
     double s0 = 0.0, s1 = 0.0;

@@ -145,8 +145,9 @@ struct Q8At {
     uint8_t* scales;   // two bytes per block: exp_avg's, exp_avg_sq's
 };
 __device__ __forceinline__ Q8At q8_at(const Q8Entry& e) {
-    const int64_t off = (int64_t)e.off * kQ8Pad, padded = (int64_t)e.padded * kQ8Pad;
-    return Q8At{e.state + 2 * off, e.state + 2 * padded + off / (kQ8Block / 2)};
+    uint8_t* const state = unpack_ptr<uint8_t>(e.lo[2], e.hi[1]);
+    const int64_t off = (int64_t)(e.index_off >> 24) * kLaunchElems, padded = (int64_t)e.padded * kQ8Pad;
+    return Q8At{state + 2 * off, state + 2 * padded + off / (kQ8Block / 2)};
 }
 
 }  // namespace zs

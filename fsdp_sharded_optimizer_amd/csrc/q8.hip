@@ -34,7 +34,7 @@ constexpr unsigned kDecodeLds = 8192;
 
 // Where a wave works: its tensor's entry and its chunk.
 struct Chunk {
-    const Q8Entry& e;
+    Q8Entry e;
     int64_t first;     // of the entry, of the chunk's elements
     int64_t i;         // of the lane's first block's elements
     uint8_t* m;        // the lane's codes
@@ -43,7 +43,7 @@ struct Chunk {
 };
 __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
     uint32_t first_tile;
-    const Q8Entry& e = b.e[find_tensor(b.tab, blockIdx.x, first_tile)];
+    const Q8Entry e = b.e[find_tensor(b.tab, blockIdx.x, first_tile)];
     const Q8At at = q8_at(e);
     const int64_t first = (int64_t)(blockIdx.x - first_tile) * kQ8Pad;
     return Chunk{e, first, first + threadIdx.x * 4,
@@ -107,9 +107,9 @@ __device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, cons
     const uint32_t e = q8_scale(wave_max8(most));
     uint32_t mc[kBlocks], vc[kBlocks];
     uint32_t scales[2] = {0, 0};
-    const uint32_t tensor_key = q8_mix(key + c.e.index * kGolden);
+    const uint32_t tensor_key = q8_mix(key + (c.e.index_off & 0xFFFFFFu) * kGolden);
     // the chunk's first group; its 256 groups share the upper 32 bits
-    const uint32_t group = q8_group(((uint64_t)c.e.off * kQ8Pad + (uint64_t)c.first) / 4, tensor_key);
+    const uint32_t group = q8_group(((uint64_t)(c.e.index_off >> 24) * kLaunchElems + (uint64_t)c.first) / 4, tensor_key);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
         const uint32_t em = (uint32_t)__builtin_amdgcn_readlane((int)e, max8_lane(2 * b));
@@ -148,8 +148,9 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
     using P = typename GradType<PBF16>::T;
     using G = typename GradType<GBF16>::T;
     const int64_t n = c.e.numel;
-    P* const param = static_cast<P*>(c.e.param);
-    const G* const grad = static_cast<const G*>(c.e.grad);
+    P* const param = unpack_ptr<P>(c.e.lo[0], c.e.hi[0]);
+    const G* const grad = unpack_ptr<const G>(c.e.lo[1], c.e.hi[0] >> 16);
+    uint16_t* const copy = unpack_ptr<uint16_t>(c.e.lo[3], c.e.hi[1] >> 16);
     float g[kBlocks][4], p[kBlocks][4], m[kBlocks][4], v[kBlocks][4];
     uint32_t mc[kBlocks], vc[kBlocks];
 #pragma unroll
@@ -198,8 +199,7 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
             if (!WHOLE && c.i + k * kQ8Block + j >= n) m[k][j] = v[k][j] = 0.0f;
         }
         store4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
-        if (!PBF16 && c.e.copy != nullptr)
-            store4(static_cast<uint16_t*>(c.e.copy), c.i + k * kQ8Block, n, WHOLE, p[k]);
+        if (!PBF16 && copy != nullptr) store4(copy, c.i + k * kQ8Block, n, WHOLE, p[k]);
     }
     store_moments(c, sc.key, m, v);
 }
@@ -218,12 +218,14 @@ __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
     const Chunk c = chunk_of(b);
     const int64_t n = c.e.numel;
     const bool whole = c.first + kQ8Pad <= n;
+    const T* const from_m = unpack_ptr<const T>(c.e.lo[0], c.e.hi[0]);
+    const T* const from_v = unpack_ptr<const T>(c.e.lo[1], c.e.hi[0] >> 16);
     float m[kBlocks][4] = {}, v[kBlocks][4] = {};
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
         const int64_t i = c.i + k * kQ8Block;
-        if (c.e.param != nullptr) load4(static_cast<const T*>(c.e.param), i, n, whole, m[k]);
-        if (c.e.grad != nullptr) load4(static_cast<const T*>(c.e.grad), i, n, whole, v[k]);
+        if (from_m != nullptr) load4(from_m, i, n, whole, m[k]);
+        if (from_v != nullptr) load4(from_v, i, n, whole, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)
@@ -244,8 +246,8 @@ __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     uint2 scales = *c.scales;
     scales.x = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.x);
     scales.y = (uint32_t)__builtin_amdgcn_readfirstlane((int)scales.y);
-    T* const m = static_cast<T*>(c.e.param);
-    T* const v = static_cast<T*>(c.e.copy);
+    T* const m = unpack_ptr<T>(c.e.lo[0], c.e.hi[0]);
+    T* const v = unpack_ptr<T>(c.e.lo[1], c.e.hi[0] >> 16);
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
         const int64_t i = c.i + k * kQ8Block;

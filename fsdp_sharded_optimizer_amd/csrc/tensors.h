@@ -6,24 +6,27 @@
 
 namespace zs {
 
-// One launch covers up to kListMax tensors.  A tensor's elements are cut in
-// tiles; workgroups are laid out tensor after tensor, and tile_start[t] is the
-// first workgroup of tensor t (every entry past the last is UINT32_MAX).
-// coarse[g] repeats tile_start[8g], so a workgroup finds its tensor with two
-// rounds of scalar loads (8 coarse entries, then 8 fine ones) and then reads
-// its record: three dependent scalar loads, against six or seven for a
-// bisection, and a fourth of the comparisons of a scan over all 64.
-constexpr int kListMax = 64;
+// One launch covers up to N tensors.  A tensor's elements are cut in tiles;
+// workgroups are laid out tensor after tensor, and tile_start[t] is the first
+// workgroup of tensor t (every entry past the last is UINT32_MAX).  coarse[g]
+// repeats tile_start[8 g], so a workgroup finds its tensor with two rounds of
+// scalar loads (the coarse entries, then 8 fine ones) and then reads its record:
+// three dependent scalar loads, against six or seven for a bisection, and a
+// fifth of the comparisons of a scan over all.
 constexpr int kListGroup = 8;
+template <int N>
 struct ListTable {
-    uint32_t coarse[kListMax / kListGroup];
-    uint32_t tile_start[kListMax];
+    static constexpr int kMax = N;
+    static constexpr int kGroups = (N + kListGroup - 1) / kListGroup;
+    uint32_t coarse[kGroups];
+    uint32_t tile_start[kGroups * kListGroup];
 };
 
-__device__ __forceinline__ int find_tensor(const ListTable& tab, uint32_t w, uint32_t& first) {
+template <int N>
+__device__ __forceinline__ int find_tensor(const ListTable<N>& tab, uint32_t w, uint32_t& first) {
     int g = 0;
 #pragma unroll
-    for (int k = 1; k < kListMax / kListGroup; ++k) g += w >= tab.coarse[k] ? 1 : 0;
+    for (int k = 1; k < ListTable<N>::kGroups; ++k) g += w >= tab.coarse[k] ? 1 : 0;
     const int at = g * kListGroup;
     int t = at;
     first = tab.tile_start[at];
@@ -36,6 +39,18 @@ __device__ __forceinline__ int find_tensor(const ListTable& tab, uint32_t w, uin
     }
     return t;
 }
+
+// A device address in 48 bits: its low word, and its upper 16 bits as one half
+// of a word.  A record of five pointers and a length is then 36 bytes, and the 4
+// KiB of kernel arguments hold 98 of them (the 291 tensors of a 7B model: 3
+// launches; with whole pointers 64, and 5 launches).
+template <typename T>
+__device__ __forceinline__ T* unpack_ptr(uint32_t lo, uint32_t hi16) {
+    return reinterpret_cast<T*>((uint64_t)(hi16 & 0xFFFFu) << 32 | lo);
+}
+inline bool packable(const void* p) { return (reinterpret_cast<uintptr_t>(p) >> 48) == 0; }
+inline uint32_t ptr_lo(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p); }
+inline uint32_t ptr_hi(const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) >> 32); }
 
 // --- accesses at any element alignment -------------------------------------
 // gfx950 serves vector accesses at any byte address; the types tell the
@@ -82,13 +97,13 @@ constexpr int64_t kListMaxTiles = (int64_t(1) << 32) / 256 - 1;
 
 // --- the squared norm -----------------------------------------------------
 struct NormEntry {
-    const void* grad;
-    int64_t numel;
+    uint32_t lo, hi, numel;
 };
 struct NormBatch {
-    ListTable tab;
-    NormEntry e[kListMax];
+    ListTable<240> tab;
+    NormEntry e[240];
 };
+static_assert(sizeof(NormBatch) <= 4072, "kernel arguments");
 int64_t norm_tile_elems(int grad_bf16);   // elements per workgroup (one binary64 partial each)
 hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, int64_t tiles, float scale, double* partials,
                                hipStream_t stream);
@@ -98,20 +113,16 @@ hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, int64_t tiles,
 // other tiles start on cache lines of every stream that is read and written
 // (0 where the tensor's streams do, or cannot all).
 struct AdamwEntry {
-    void* param;
-    const void* grad;
-    float* exp_avg;
-    float* exp_avg_sq;
-    uint16_t* copy;     // bf16 re-cast of an fp32 param, nullable
+    uint32_t lo[5];   // param, grad, exp_avg, exp_avg_sq, bf16 re-cast (0: none)
+    uint32_t hi[3];   // param | grad << 16, exp_avg | exp_avg_sq << 16, re-cast | shift << 16
     uint32_t numel;
-    uint32_t shift;
 };
 struct AdamwBatch {
-    ListTable tab;
-    AdamwScalars sc;             // unless sc_dev is set
+    ListTable<98> tab;
+    AdamwEntry e[98];
     const AdamwScalars* sc_dev;
     const double* norm_sq;       // nullable
-    AdamwEntry e[kListMax];
+    AdamwScalars sc;             // unless sc_dev is set
 };
 constexpr int64_t kListTile = 256;
 static_assert(sizeof(AdamwBatch) <= 4096, "kernel arguments");
@@ -132,26 +143,25 @@ struct Q8Scalars {   // zs_adamw_q8_scalars
     uint32_t reserved;
 };
 
-// `off` elements of the tensor come before the entry's first, `padded` is the
-// whole tensor's padded length (both in units of kQ8Pad); `state` is the whole
-// tensor's buffer, the other pointers the entry's.  `index` is the tensor's
-// place in the caller's list.
+// `off` elements of the tensor come before the entry's first, in units of
+// kLaunchElems; `padded` is the whole tensor's padded length in units of kQ8Pad;
+// the state is the whole tensor's buffer, the other pointers the entry's.  The
+// index is the tensor's place in the caller's list.
+constexpr int32_t kQ8MaxCount = 1 << 24;
 struct Q8Entry {
-    void* param;        // encode: exp_avg source; decode: exp_avg destination (nullable)
-    const void* grad;   // encode: exp_avg_sq source
-    uint8_t* state;
-    void* copy;         // the step's bf16 re-cast; decode: exp_avg_sq destination (nullable)
+    uint32_t lo[4];       // step: param, grad, state, bf16 re-cast (0: none);
+                          // conversions: exp_avg, exp_avg_sq (0: none), state
+    uint32_t hi[2];       // the first | the second << 16, state | re-cast << 16
     uint32_t numel;
-    uint32_t off;
+    uint32_t index_off;   // index | off << 24
     uint32_t padded;
-    uint32_t index;
 };
 struct Q8Batch {
-    ListTable tab;
-    Q8Scalars sc;                // the conversions use the key alone
+    ListTable<98> tab;
+    Q8Entry e[98];
     const Q8Scalars* sc_dev;
     const double* norm_sq;       // nullable
-    Q8Entry e[kListMax];
+    Q8Scalars sc;                // the conversions use the key alone
 };
 static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream);

@@ -6,9 +6,10 @@
  * tensors, as a model that is not flattened has them: the squared gradient
  * norm over the list, the AdamW update of every tensor with its moments in
  * fp32 or in 8 bits, and the conversions of 8-bit moments.  The list is read
- * during the call only: tables of it travel in the kernel arguments, 64
- * tensors to a launch, so nothing is allocated, copied to the device or kept,
- * and a call can be captured into a HIP graph as is.
+ * during the call only: tables of it travel in the kernel arguments (98
+ * tensors to a launch, 240 for the norm), so nothing is allocated on the
+ * device, copied to it or kept, and a call can be captured into a HIP graph as
+ * is.
  *
  * For every call: count >= 0 and the list not NULL with count > 0; a tensor's
  * numel >= 0, the sum at most 2^39; a tensor with numel 0 is skipped (its
@@ -71,7 +72,7 @@ typedef struct {
  * for bit those of that call on each tensor (its gradient widened to fp32).
  * hp and norm_sq_dev as there: one clip coefficient for the whole list, and a
  * non-finite norm leaves every tensor unchanged.
- * Errors: ZS_EINVAL, ZS_EOVERLAP, ZS_EHIP (lists of more than 64 tensors are
+ * Errors: ZS_EINVAL, ZS_EOVERLAP, ZS_EHIP (lists of more than 98 tensors are
  * several launches: a failed one leaves the earlier ones enqueued).
  */
 ZS_API int32_t adamw_step_tensors(const zs_adamw* hp, const zs_adamw_tensor* tensors, int32_t count,

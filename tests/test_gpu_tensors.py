@@ -22,9 +22,9 @@ pytestmark = pytest.mark.gpu
 LISTS = {
     "one": [1],
     "edges": [1, 2, 3, 4, 5, 63, 64, 255, 256, 257, 0, 511, 1023, 1024, 1025],
-    "many": [(37 * k) % 700 for k in range(150)],          # zeros among them, three launches
-    "sixty-four": [256] * 64,
-    "sixty-five": [300] * 65,
+    "many": [(37 * k) % 700 for k in range(250)],          # zeros among them; three launches, two for the norm
+    "one table": [256] * 98,
+    "a table and one": [300] * 99,
     "large": [1_000_003, 7, 262_144],
 }
 GUARD = 17        # elements on each side
