@@ -121,14 +121,21 @@ public:
             if (rc != ZS_OK) return rc;
         }
         out = count_;
-        b_.tab.tile_start[count_] = (uint32_t)tiles_;
-        if (count_ % kListGroup == 0) b_.tab.coarse[count_ / kListGroup] = (uint32_t)tiles_;
-        ++count_;
+        b_.tab.start[count_++] = (uint32_t)tiles_;
         tiles_ += tiles;
         return ZS_OK;
     }
     int32_t flush() {
         if (count_ == 0) return ZS_OK;
+        auto& tab = b_.tab;
+        tab.shift = 0;
+        while (((tiles_ - 1) >> tab.shift) >= kListBuckets) ++tab.shift;
+        std::memset(tab.bucket, 0, sizeof(tab.bucket));
+        int t = 0;
+        for (int part = 0; part < kListBuckets && ((int64_t)part << tab.shift) < tiles_; ++part) {
+            while ((int64_t)tab.start[t + 1] <= ((int64_t)part << tab.shift)) ++t;
+            tab.bucket[part / 4] |= (uint32_t)t << (8 * (part % 4));
+        }
         const int32_t rc = hip_status(launch_(b_, tiles_));
         clear();
         return rc;
@@ -136,7 +143,8 @@ public:
 
 private:
     void clear() {
-        std::memset(&b_.tab, 0xFF, sizeof(b_.tab));
+        static_assert(decltype(b_.tab)::kMax <= 255, "a bucket names a tensor in a byte");
+        for (uint32_t& s : b_.tab.start) s = kNoTile;
         count_ = 0;
         tiles_ = 0;
     }
