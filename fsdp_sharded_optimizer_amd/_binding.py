@@ -218,10 +218,11 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None) -> int:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    if s.device.index != torch.cuda.current_device():
-        raise ValueError(f"stream on {s.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return int(s.cuda_stream)
+    if stream is None:   # the current stream's handle, without a Stream object around it (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream on {stream.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return int(stream.cuda_stream)
 
 
 def _norm(norm_sq: Optional[torch.Tensor], fn: str) -> int:

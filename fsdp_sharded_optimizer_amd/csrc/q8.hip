@@ -27,10 +27,15 @@ constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per wave
 // 8 KiB, 68.2 at 12; storing 68.1 % uncapped, 70.3 at 4 KiB, 60.4 at 6.  Two blocks
 // per wave instead of four: the step within 0.3 points at its best cap, storing
 // 4 points slower; 2 or 4 waves per workgroup: 0.5-4 points slower; plain instead
-// of streaming code accesses: the step 1 point slower.
+// of streaming code accesses: the step 1 point slower.  A launch of fewer than
+// 32768 chunks (34M elements) is not long enough for that and ends sooner with
+// more of it resident: 8.4M bf16 parameters 19.6 us uncapped, 21.2 at 10 KiB; 34M
+// 59.0 and 61.0; read out 10.4 and 10.9 at 8 KiB.
 template <bool PBF16> constexpr unsigned kStepLds = PBF16 ? 10240 : 14336;
 constexpr unsigned kEncodeLds = 4096;
 constexpr unsigned kDecodeLds = 8192;
+constexpr int64_t kCapChunks = 32768;
+unsigned cap(unsigned lds, int64_t chunks) { return chunks < kCapChunks ? 0 : lds; }
 
 // Where a wave works: its tensor's entry and its chunk.
 struct Chunk {
@@ -267,9 +272,9 @@ template <bool PBF16, bool GBF16>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, kStepLds<PBF16>, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, cap(kStepLds<PBF16>, tiles), stream, b);
     else
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, kStepLds<PBF16>, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, cap(kStepLds<PBF16>, tiles), stream, b);
     return hipGetLastError();
 }
 
@@ -283,15 +288,15 @@ hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int6
 
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, kEncodeLds, stream, b);
-    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, kEncodeLds, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, cap(kEncodeLds, tiles), stream, b);
+    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, cap(kEncodeLds, tiles), stream, b);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, kDecodeLds, stream, b);
-    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, kDecodeLds, stream, b);
+    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, cap(kDecodeLds, tiles), stream, b);
+    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, cap(kDecodeLds, tiles), stream, b);
     return hipGetLastError();
 }
 
