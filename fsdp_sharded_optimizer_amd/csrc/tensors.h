@@ -140,9 +140,9 @@ hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf
 // --- 8-bit moments --------------------------------------------------------
 // Layout of one tensor's buffer of n elements, P = n rounded up to kQ8Pad:
 // 2 P bytes of codes (their order is in q8.h), then two bytes per block (exp_avg's
-// e, exp_avg_sq's e).  A workgroup takes kQ8Pad elements.
+// e, exp_avg_sq's e).
 constexpr int64_t kQ8Block = 256;
-constexpr int64_t kQ8Pad = 1024;
+constexpr int64_t kQ8Pad = 512;
 __host__ __device__ __forceinline__ int64_t q8_padded(int64_t n) { return (n + kQ8Pad - 1) / kQ8Pad * kQ8Pad; }
 
 struct Q8Scalars {   // zs_adamw_q8_scalars
@@ -172,8 +172,10 @@ struct Q8Batch {
     Q8Scalars sc;                // the conversions use the key alone
 };
 static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
+// the conversions' elements per workgroup, for a list of that many in all
+int64_t q8_encode_tile(int64_t total);
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream);
-hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
+hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
 
 }  // namespace zs
