@@ -393,8 +393,9 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
     NormBatch b;
     std::memset(&b, 0, sizeof(b));
     auto launch = [&](const NormBatch& x, int64_t tiles) {
-        const hipError_t e = launch_norm_tensors(x, grad_dtype == ZS_BF16, tiles, (float)grad_scale, partials + done,
-                                                 as_stream(hip_stream));
+        // a list of one tile: its partial is the result
+        const hipError_t e = launch_norm_tensors(x, grad_dtype == ZS_BF16, tiles, (float)grad_scale,
+                                                 parts == 1 ? out_sq_dev : partials + done, as_stream(hip_stream));
         done += tiles;
         return e;
     };
@@ -410,7 +411,7 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
             b.e[at] = NormEntry{ptr_lo(p), ptr_hi(p), (uint32_t)n};
         }
     const int32_t rc = fill.flush();
-    if (rc != ZS_OK) return rc;
+    if (rc != ZS_OK || parts == 1) return rc;
     return hip_status(launch_sum_partials(partials, parts, partials + parts, out_sq_dev, as_stream(hip_stream)));
 }
 

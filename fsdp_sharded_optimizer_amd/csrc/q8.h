@@ -85,18 +85,28 @@ __device__ __forceinline__ void q8_unpack4(uint32_t codes, float (&x)[4]) {
     for (int j = 0; j < 4; ++j) {
         // exp_avg: the code's sign, extended, ends in bit 31; its 7 other bits in 26..20
         if constexpr (TOP == kTopM)
-            x[j] = __uint_as_float(((uint32_t)(int32_t)(int8_t)(codes >> (8 * j)) << 20) & 0x87F00000u);
+            x[j] = __uint_as_float(((uint32_t)__builtin_amdgcn_sbfe((int)codes, 8 * j, 8) << 20) & 0x87F00000u);
         else
-            x[j] = __uint_as_float(((codes >> (8 * j)) & 0xFFu) << 20);
+            x[j] = __uint_as_float(__builtin_amdgcn_ubfe(codes, 8 * j, 8) << 20);
     }
 }
 
-// The values of 4 codes in a word; e: their block's scale byte.
+// Unpacked codes into values; e: their block's scale byte.
+template <int TOP>
+__device__ __forceinline__ void q8_scale4(uint32_t e, float (&x)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = e == 255u ? __builtin_nanf("") : __builtin_ldexpf(x[j], (int)e - TOP);
+}
 template <int TOP>
 __device__ __forceinline__ void q8_decode4(uint32_t codes, uint32_t e, float (&x)[4]) {
     q8_unpack4<TOP>(codes, x);
+    if (plain_scale<TOP>(e)) {
+        const float scale = exp2_of((int)e - TOP);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = e == 255u ? __builtin_nanf("") : __builtin_ldexpf(x[j], (int)e - TOP);
+        for (int j = 0; j < 4; ++j) x[j] = x[j] * scale;
+    } else {
+        q8_scale4<TOP>(e, x);
+    }
 }
 
 // the top bytes of four words, the first one's lowest

@@ -21,16 +21,17 @@ namespace {
 constexpr int kWave = 64;
 constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per chunk
 // LDS reserved (never touched) per workgroup to cap how many share a CU: too
-// many keep too many DRAM rows open.  % of the 8 TB/s peak at 0 / 3 / 4 / 5 / 6 / 7 /
-// 8 / 9 / 10 KiB: the step on 809M fp32 parameters (bf16 gradients, re-casts) 75.2 /
-// . / . / . / 76.2 / 79.0 / 79.7 / 80.3 / 80.3; on 855M bf16 parameters 80.4 / 80.4 /
-// 80.4 / 80.4 / 78.5 / 75.0 (5 KiB are 32 waves per CU, as many as it takes: no cap);
-// reading 855M moments out 79.6 / 79.6 / 79.5 / 79.6 / 80.8; storing 317M 71.1 at
-// 0-5 KiB, 61.2 at 6.  (2 or 4 waves per workgroup: 0.5-4 points slower; plain
-// instead of streaming code accesses: the step 1 point slower.)  Launches of
-// fewer than 2^25 elements are not long enough for a cap to help.
-constexpr unsigned kStepLdsF32 = 9216;
+// many keep too many DRAM rows open.  % of the 8 TB/s peak at 0-5 (32 waves per
+// CU, all it takes) / 6 / 7 / 8 / 9 / 11 / 12 KiB: the step on 809M fp32 parameters
+// (bf16 gradients, re-casts) 74.3 / 76.7 / 77.5 / 78.9 / 79.8 / 79.0 / 75.7; on 855M
+// bf16 parameters 79.7 / 80.7 / 81.4 / 79.5 / 77.4 / 73.3 / 67.1; reading 855M moments
+// out 80.2 / 80.9 / 78.1 / 74.2 / 69.1; storing 317M 69.3 at 0, 71.4 at 5, 61.4 at 6.
+// (2 or 4 waves per workgroup: 0.5-4 points slower; plain instead of streaming
+// code accesses: the step 1 point slower.)  Launches of fewer than 2^25 elements
+// are not long enough for a cap to help.
+template <bool PBF16> constexpr unsigned kStepLds = PBF16 ? 7168 : 9216;
 constexpr unsigned kDecodeLds = 6144;
+constexpr unsigned kEncodeLds = 5120;
 constexpr int64_t kCapElems = int64_t(1) << 25;
 unsigned cap(unsigned lds, int64_t elems) { return elems < kCapElems ? 0 : lds; }
 
@@ -88,6 +89,11 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[kBloc
 __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[kBlocks]) {
     st_stream(reinterpret_cast<u32x2*>(p), u32x2{w[0], w[1]});
 }
+
+// Until every load of the wave has come: a wave that reads all it needs before it
+// writes anything lets DRAM turn from reads to writes less often (reading 855M
+// moments out: 77.5 % of the HBM peak without, 80.2 % with).
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0)
 
 // A chunk's scale bytes as a word: block b's exp_avg byte and exp_avg_sq byte are
 // the bytes 2b and 2b + 1.
@@ -172,21 +178,20 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
     if (!clip_coef(sc.adamw, b.norm_sq, coef)) return;
     scales = uniform(scales);
     const AdamwScalars& a = sc.adamw;
-    const float inv_root = 1.0f / a.bias_correction2_sqrt;
+    const float inv_root = __builtin_amdgcn_rcpf(a.bias_correction2_sqrt);
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
         const uint32_t em = scale_m(scales, k), ev = scale_v(scales, k);
         // beta * value: the scale, a power of two, goes into the factor, which
         // changes no bit of the product
-        float keep_m = a.beta1, keep_v = a.beta2;
-        if (plain_scale<kTopM>(em) && plain_scale<kTopV>(ev)) {
-            q8_unpack4<kTopM>(mc[k], m[k]);
-            q8_unpack4<kTopV>(vc[k], v[k]);
-            keep_m *= exp2_of((int)em - kTopM);
-            keep_v *= exp2_of((int)ev - kTopV);
-        } else {
-            q8_decode4<kTopM>(mc[k], em, m[k]);
-            q8_decode4<kTopV>(vc[k], ev, v[k]);
+        q8_unpack4<kTopM>(mc[k], m[k]);
+        q8_unpack4<kTopV>(vc[k], v[k]);
+        float keep_m = a.beta1 * exp2_of((int)em - kTopM), keep_v = a.beta2 * exp2_of((int)ev - kTopV);
+        if (!plain_scale<kTopM>(em) || !plain_scale<kTopV>(ev)) {
+            q8_scale4<kTopM>(em, m[k]);
+            q8_scale4<kTopV>(ev, v[k]);
+            keep_m = a.beta1;
+            keep_v = a.beta2;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[k][j] = g[k][j] * a.grad_scale;
@@ -251,10 +256,10 @@ __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     uint32_t mc[kBlocks], vc[kBlocks];
     load_codes(c.codes, mc);
     load_codes(c.codes + kQ8Pad, vc);
-    uint32_t scales = load_scales(c.scales);
-    scales = uniform(scales);
+    const uint32_t scales = uniform(load_scales(c.scales));
     T* const m = unpack_ptr<T>(c.e.lo[0], c.e.hi[0]);
     T* const v = unpack_ptr<T>(c.e.lo[1], c.e.hi[0] >> 16);
+    wait_loads();
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
         const int64_t i = c.i + k * kQ8Block;
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
 template <bool PBF16, bool GBF16>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    const unsigned lds = PBF16 ? 0 : cap(kStepLdsF32, tiles * kQ8Pad);
+    const unsigned lds = cap(kStepLds<PBF16>, tiles * kQ8Pad);
     if (b.sc_dev != nullptr)
         hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, lds, stream, b);
     else
@@ -293,12 +298,12 @@ template <bool BF16>
 static hipError_t encode(const Q8Batch& b, int64_t tile, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     if (tile == kQ8Pad) hipLaunchKernelGGL((q8_encode_kernel<BF16, 1>), grid, block, 0, stream, b);
-    else hipLaunchKernelGGL((q8_encode_kernel<BF16, 2>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((q8_encode_kernel<BF16, 2>), grid, block, kEncodeLds, stream, b);
     return hipGetLastError();
 }
 
-// Two chunks per wave for long lists: 317M moments stored in 335 us, 364 with one
-// (up to 34M elements one is as fast, and faster below 4M).
+// Two chunks per wave for long lists: 317M moments stored in 333 us, 352 with one
+// (one is as fast up to 34M elements, and faster below 4M).
 int64_t q8_encode_tile(int64_t total) { return total < kCapElems ? kQ8Pad : 2 * kQ8Pad; }
 
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t tiles, hipStream_t stream) {
@@ -307,8 +312,9 @@ hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t ti
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, cap(kDecodeLds, tiles * kQ8Pad), stream, b);
-    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, cap(kDecodeLds, tiles * kQ8Pad), stream, b);
+    const unsigned lds = cap(kDecodeLds, tiles * kQ8Pad);
+    if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, lds, stream, b);
+    else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, lds, stream, b);
     return hipGetLastError();
 }
 

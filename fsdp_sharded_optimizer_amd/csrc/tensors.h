@@ -54,7 +54,10 @@ __device__ __forceinline__ uint32_t find_tensor(const ListTable<N>& tab, uint32_
 // launches; with whole pointers 64, and 5 launches).
 template <typename T>
 __device__ __forceinline__ T* unpack_ptr(uint32_t lo, uint32_t hi16) {
-    return reinterpret_cast<T*>((uint64_t)(hi16 & 0xFFFFu) << 32 | lo);
+    // global memory, said so: accesses through a pointer made from an integer
+    // are flat ones otherwise, which also wait for LDS
+    typedef __attribute__((address_space(1))) T Global;
+    return (T*)(Global*)((uint64_t)(hi16 & 0xFFFFu) << 32 | lo);
 }
 inline bool packable(const void* p) { return (reinterpret_cast<uintptr_t>(p) >> 48) == 0; }
 inline uint32_t ptr_lo(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p); }
@@ -172,7 +175,8 @@ struct Q8Batch {
     Q8Scalars sc;                // the conversions use the key alone
 };
 static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
-// the conversions' elements per workgroup, for a list of that many in all
+// elements per workgroup of the storing conversion, for a list of that many in
+// all (the step and the reading one: kQ8Pad)
 int64_t q8_encode_tile(int64_t total);
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t tiles, hipStream_t stream);
