@@ -41,6 +41,9 @@ Over lists of tensors (include/zshard_tensors.h), each list marshalled once:
     adamw_step_tensors_q8(hp, tensors, seed=0, norm_sq=None)    8-bit moments; _dev: q8_scalars_bytes(hp, seed)
     moments_q8_bytes(n) / moments_q8_encode(moments, seed=0) / moments_q8_decode(moments)
 
+TensorOptimizer(params, lr=..., state_bits=32 or 8) orders them, as
+ShardOptimizer does the calls over a flat shard.
+
 DeviceArena(nbytes, device) holds one physically contiguous block of device
 memory and hands out 2 MiB-aligned views of it (ShardOptimizer(arena=...)).
 
@@ -93,6 +96,7 @@ from ._binding import (  # noqa: F401
 )
 from .arena import DeviceArena  # noqa: F401
 from .step import ShardOptimizer  # noqa: F401
+from .tensor_step import TensorOptimizer  # noqa: F401
 from .tensors import (  # noqa: F401
     Q8_BLOCK,
     TENSOR_EXPORTS,

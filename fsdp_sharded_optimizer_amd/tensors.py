@@ -112,6 +112,16 @@ class _List:
             setattr(self.array[k], field, p)
         self.tensors[field] = list(ts) if ts is not None else None
 
+    def clone(self) -> "_List":
+        """The list as it is now (the same tensors): later set_grads on either
+        leave the other alone."""
+        out = object.__new__(type(self))
+        out.__dict__.update(self.__dict__)
+        out.array = type(self.array).from_buffer_copy(self.array)
+        out.address = ctypes.addressof(out.array)
+        out.tensors = dict(self.tensors)
+        return out
+
     def check(self, fn: str) -> None:
         if self.count and self.device.index != torch.cuda.current_device():
             raise ValueError(f"{fn}: list on {self.device}, but the current device is "
