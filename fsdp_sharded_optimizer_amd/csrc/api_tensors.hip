@@ -262,6 +262,16 @@ int32_t add_q8(Q8Batch& batch, Fill& fill, int64_t tile, void* state, int64_t nu
     return ZS_OK;
 }
 
+// Counts the elements whose written streams start off a cache line: tiles are
+// taken in runs where they are most of a list.
+struct OffLine {
+    int64_t elems = 0;
+    void add(int64_t numel, const void* a, const void* b) {
+        if (!aligned(a, kLine) || !aligned(b, kLine)) elems += numel;
+    }
+    uint32_t runs(int64_t total) const { return elems > total / 2 ? 1 : 0; }
+};
+
 int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_scalars* sc_dev,
                         const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                         const double* norm_sq_dev, void* hip_stream) {
@@ -275,6 +285,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
     }
     const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
     Ranges ranges;
+    OffLine off_line;
     if (!ranges.reserve(count, 4)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
@@ -288,6 +299,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         ranges.add(1, t.grad, t.numel * gsz, false);
         ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), true);
         ranges.add(3, t.param_bf16, t.numel * 2, true);
+        off_line.add(t.numel, t.param, t.param_bf16);
     }
     ranges.add_read(norm_sq_dev, 8);
     ranges.add_read(sc_dev, (int64_t)sizeof(zs_adamw_q8_scalars));
@@ -299,6 +311,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         b.sc.adamw = make_scalars(hp);
         b.sc.key = q8_key(seed, hp->step);
     }
+    b.runs = off_line.runs(total);
     b.sc_dev = reinterpret_cast<const Q8Scalars*>(sc_dev);
     b.norm_sq = norm_sq_dev;
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
@@ -320,6 +333,7 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
     if (total < 0 || !dtype_ok(dtype) || count > kQ8MaxCount) return ZS_EINVAL;
     const int64_t sz = elem_size(dtype), tile = encode ? q8_encode_tile(total) : kQ8Pad;
     Ranges ranges;
+    OffLine off_line;
     if (!ranges.reserve(count, 3)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
@@ -330,10 +344,12 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
         ranges.add(0, t.exp_avg, t.numel * sz, !encode);
         ranges.add(1, t.exp_avg_sq, t.numel * sz, !encode);
         ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), encode);
+        if (!encode) off_line.add(t.numel, t.exp_avg, t.exp_avg_sq);
     }
     if (ranges.clash()) return ZS_EOVERLAP;
     Q8Batch b;
     std::memset(&b, 0, sizeof(b));
+    b.runs = off_line.runs(total);
     b.sc.key = q8_key(seed, 0);
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
         return encode ? launch_q8_encode(x, dtype == ZS_BF16, tile, tiles, as_stream(hip_stream))

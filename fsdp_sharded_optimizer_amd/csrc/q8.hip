@@ -45,10 +45,11 @@ struct Chunk {
 };
 template <int CHUNKS>
 __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
+    const uint32_t w = b.runs ? tile_in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     uint32_t first_tile;
-    const Q8Entry e = b.e[find_tensor(b.tab, blockIdx.x, first_tile)];
+    const Q8Entry e = b.e[find_tensor(b.tab, w, first_tile)];
     const Q8At at = q8_at(e);
-    const int64_t first = (int64_t)(blockIdx.x - first_tile) * (CHUNKS * kQ8Pad);
+    const int64_t first = (int64_t)(w - first_tile) * (CHUNKS * kQ8Pad);
     return Chunk{e, first, first + threadIdx.x * 4, at.codes + 2 * first + threadIdx.x * (4 * kBlocks),
                  at.scales + first / (kQ8Block / 2)};
 }
