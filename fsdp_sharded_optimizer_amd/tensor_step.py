@@ -101,7 +101,7 @@ class TensorOptimizer:
         if lst.numels != [p.numel() for p in self.params]:
             raise ValueError("bind_grads: one gradient per parameter, of its size")
         for _, at, group in self._groups:
-            group.set_grads([grads[k] for k in at])
+            group._take_grads(lst, at)
         need = zt.grad_norm_sq_tensors_workspace_bytes(lst)
         if need > self._workspace.numel():
             self._workspace = torch.empty(need, dtype=torch.uint8, device=self.norm_sq.device)

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence, Union
 
+import numpy as np
 import torch
 
 from . import _binding as zs
@@ -73,23 +74,26 @@ def _lib() -> ctypes.CDLL:
 
 def _pointers(ts: Sequence[Optional[torch.Tensor]], name: str, numels: Sequence[int], dtypes, optional: bool = False):
     """Device pointers of one kind of tensor, and their common dtype (None
-    where every tensor is None)."""
+    where every tensor is None).  One pass with the checks of zs._dev, which is
+    called only to say what is wrong: a list is some hundred tensors."""
     if len(ts) != len(numels):
         raise ValueError(f"{name}: {len(ts)} tensors, the list has {len(numels)}")
-    kind, out = None, []
+    kind, out, device = None, [], torch.cuda.current_device() if torch.cuda.is_available() else -1
     for k, (t, n) in enumerate(zip(ts, numels)):
         if t is None and optional:
             out.append(0)
             continue
-        at = zs._dev(t, f"{name}[{k}]") if t is not None else None
-        if at is None:
+        if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{k}]: expected a torch.Tensor")
-        if t.dtype not in dtypes or (kind is not None and t.dtype != kind):
+        if not t.is_cuda or t.get_device() != device or not t.is_contiguous():
+            zs._dev(t, f"{name}[{k}]")
+        if kind is None:
+            kind = t.dtype
+        if t.dtype != kind or kind not in dtypes:
             raise TypeError(f"{name}[{k}]: {t.dtype}; one of {', '.join(map(str, dtypes))}, the same for all")
         if t.numel() != n:
             raise ValueError(f"{name}[{k}]: size mismatch")
-        kind = t.dtype
-        out.append(at)
+        out.append(t.data_ptr())
     return out, kind
 
 
@@ -100,16 +104,14 @@ class _List:
     def __init__(self, struct, numels: Sequence[int], device):
         self.count = len(numels)
         self.numels = list(numels)
-        self.array = (struct * max(self.count, 1))()
-        self.address = ctypes.addressof(self.array)
-        for k, n in enumerate(numels):
-            self.array[k].numel = n
+        self.array = np.zeros(max(self.count, 1), dtype=np.dtype(struct))
+        self.address = self.array.ctypes.data
+        self.array["numel"][:self.count] = self.numels
         self.device = device
         self.tensors = {}
 
     def _set(self, field: str, ts, pointers) -> None:
-        for k, p in enumerate(pointers):
-            setattr(self.array[k], field, p)
+        self.array[field][:self.count] = pointers
         self.tensors[field] = list(ts) if ts is not None else None
 
     def clone(self) -> "_List":
@@ -117,8 +119,8 @@ class _List:
         leave the other alone."""
         out = object.__new__(type(self))
         out.__dict__.update(self.__dict__)
-        out.array = type(self.array).from_buffer_copy(self.array)
-        out.address = ctypes.addressof(out.array)
+        out.array = self.array.copy()
+        out.address = out.array.ctypes.data
         out.tensors = dict(self.tensors)
         return out
 
@@ -164,11 +166,19 @@ class _StepList(_List):
             pointers, _ = _pointers(param_bf16, "param_bf16", self.numels, (torch.bfloat16,), optional=True)
             self._set("param_bf16", param_bf16, pointers)
 
-    def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
+    def set_grads(self, grads: Union["GradTensors", Sequence[torch.Tensor]]) -> None:
         """Other gradients of the same sizes (fp32 or bf16, one dtype)."""
-        pointers, dtype = _pointers(grads, "grads", self.numels, _FLOATS)
-        self._set("grad", grads, pointers)
-        self.grad_dtype = zs.ZS_BF16 if dtype == torch.bfloat16 else zs.ZS_F32
+        if not isinstance(grads, GradTensors):
+            grads = GradTensors(grads)
+        self._take_grads(grads, range(grads.count))
+
+    def _take_grads(self, grads: "GradTensors", at: Sequence[int]) -> None:
+        """The tensors `at` of a checked list of gradients."""
+        at = np.fromiter(at, dtype=np.int64)
+        if [grads.numels[k] for k in at] != self.numels:
+            raise ValueError("grads: one per tensor of the list, of its size")
+        self._set("grad", [grads.tensors["ptr"][k] for k in at], grads.array["ptr"][at])
+        self.grad_dtype = grads.grad_dtype
 
 
 class AdamWTensors(_StepList):
@@ -186,18 +196,18 @@ class AdamWTensors(_StepList):
 
 
 def _states(ts, numels):
+    """Device pointers of 8-bit moments, large enough for the numels."""
     if len(ts) != len(numels):
         raise ValueError(f"states: {len(ts)} tensors, the list has {len(numels)}")
-    out = []
-    for k, (t, n) in enumerate(zip(ts, numels)):
-        at = zs._dev(t, f"states[{k}]", torch.uint8) if t is not None else None
-        if at is None:
+    for k, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
             raise TypeError(f"states[{k}]: expected a torch.Tensor")
+    pointers, _ = _pointers(ts, "states", [t.numel() for t in ts], (torch.uint8,))
+    for k, (t, n) in enumerate(zip(ts, numels)):
         if t.numel() < moments_q8_bytes(n):
             raise ValueError(f"states[{k}]: holds {t.numel()} bytes, the 8-bit moments of {n} elements need "
                              f"{moments_q8_bytes(n)}")
-        out.append(at)
-    return out
+    return pointers
 
 
 class AdamWQ8Tensors(_StepList):
