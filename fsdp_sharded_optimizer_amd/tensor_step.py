@@ -46,6 +46,18 @@ def _states_for(params: Sequence[torch.Tensor]) -> list:
     return list(buffer[:sum(sizes)].split(sizes))
 
 
+def _written(params: Sequence[torch.Tensor], copies) -> tuple:
+    """First and past-last addresses of what a step writes of the caller's, in
+    ascending order.  The library refuses overlaps inside one call; a step is a
+    call per weight decay."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                   for t in [*params, *(copies or [])] if t is not None and t.numel())
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("params and param_bf16 must not overlap")
+    lo, hi = np.array(spans, dtype=np.uint64).reshape(-1, 2).T
+    return lo, hi
+
+
 class TensorOptimizer:
     """AdamW over `params` (contiguous fp32 or bf16 GPU tensors of one dtype,
     updated in place).  param_bf16: for fp32 params, bf16 tensors (or None) that
@@ -65,6 +77,8 @@ class TensorOptimizer:
         decays = [float(weight_decay)] * len(params) if np.isscalar(weight_decay) else [float(d) for d in weight_decay]
         if len(decays) != len(params):
             raise ValueError(f"weight_decay: {len(decays)} values for {len(params)} tensors")
+        if not all(0.0 <= d < float("inf") for d in decays):
+            raise ValueError("weight_decay: finite values >= 0")
         if param_bf16 is not None and len(param_bf16) != len(params):
             raise ValueError(f"param_bf16: {len(param_bf16)} tensors for {len(params)}")
         zt.GradTensors(params)   # the tensors' checks, before anything is allocated
@@ -72,6 +86,8 @@ class TensorOptimizer:
         self.lr, self.betas, self.eps = lr, betas, eps
         self.grad_scale, self.max_norm = grad_scale, max_norm
         self.compute_norm = (max_norm > 0) if compute_norm is None else compute_norm
+        self._check_clip()
+        self._lo, self._hi = _written(params, param_bf16)
         if state_bits == 32:
             self._exp_avg, self._exp_avg_sq = _moments_like(params), _moments_like(params)
         else:
@@ -100,12 +116,22 @@ class TensorOptimizer:
         lst = zt.GradTensors(list(grads))
         if lst.numels != [p.numel() for p in self.params]:
             raise ValueError("bind_grads: one gradient per parameter, of its size")
+        # the first buffer that is written and ends after a gradient's start, if any
+        at = np.searchsorted(self._hi, lst.array["ptr"][:lst.count], side="right")
+        lo = np.append(self._lo, np.uint64(0xFFFFFFFFFFFFFFFF))[at]
+        sizes = np.array(lst.numels) * (2 if lst.grad_dtype == zs.ZS_BF16 else 4)
+        if ((lo < lst.array["ptr"][:lst.count] + sizes.astype(np.uint64)) & (sizes > 0)).any():
+            raise ValueError("bind_grads: a gradient overlaps a parameter or a re-cast")
         for _, at, group in self._groups:
             group._take_grads(lst, at)
         need = zt.grad_norm_sq_tensors_workspace_bytes(lst)
         if need > self._workspace.numel():
             self._workspace = torch.empty(need, dtype=torch.uint8, device=self.norm_sq.device)
         self._grads = lst
+
+    def _check_clip(self) -> None:
+        if self.max_norm > 0 and not self.compute_norm:
+            raise ValueError("max_norm > 0 needs the norm: compute_norm")
 
     def _hp(self, decay: float, extra_norm_sq: float, t: int) -> zs.AdamWConfig:
         return zs.AdamWConfig(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, weight_decay=decay,
@@ -122,6 +148,7 @@ class TensorOptimizer:
             self.bind_grads(grads)
         if self._grads is None:
             raise RuntimeError("step() without gradients")
+        self._check_clip()
         norm = None
         if self.compute_norm:
             norm = zt.grad_norm_sq_tensors(self._grads, self.grad_scale, self.norm_sq, self._workspace)

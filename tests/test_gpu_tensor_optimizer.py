@@ -224,3 +224,42 @@ def test_moments_sit_where_the_step_is_aligned():
         for p, m, v in zip(views, *opt.moments()):
             lane = p.data_ptr() // p.element_size() % 32
             assert m.data_ptr() // 4 % 32 == lane and v.data_ptr() // 4 % 32 == lane
+
+
+def test_no_step_is_half_refused():
+    """What one of a step's calls would refuse, or could not see, is refused
+    before the first: a bad decay, the same memory under two decays, a gradient
+    in a parameter that another call writes, clipping without the norm."""
+    p = start(torch.float32)
+    for bad in (-0.1, math.nan, math.inf):
+        with pytest.raises(ValueError):
+            zs.TensorOptimizer(p, lr=1e-3, weight_decay=[0.1, bad] + [0.1] * 4)
+    with pytest.raises(ValueError):
+        zs.TensorOptimizer([p[0], p[0]], lr=1e-3, weight_decay=[0.1, 0.0])
+    with pytest.raises(ValueError):
+        zs.TensorOptimizer([p[0], p[0].reshape(-1)[-1:]], lr=1e-3, weight_decay=[0.1, 0.0])
+    copy = p[1].view(torch.bfloat16).reshape(-1)[:16]
+    with pytest.raises(ValueError):
+        zs.TensorOptimizer(p[:2], lr=1e-3, weight_decay=[0.1, 0.0], param_bf16=[None, copy])
+    with pytest.raises(ValueError):
+        zs.TensorOptimizer(p, lr=1e-3, max_norm=1.0, compute_norm=False)
+    empty = torch.empty(0, device="cuda")
+    opt = zs.TensorOptimizer(p + [empty], lr=1e-3, weight_decay=DECAY + [0.0])
+    grads = gradients(1, torch.float32) + [empty]
+    before = [x.clone() for x in p]
+    for k in range(len(p)):   # the parameter of another call, whole or only its last element
+        with pytest.raises(ValueError):
+            opt.step(grads[:k] + [p[k]] + grads[k + 1:])
+    with pytest.raises(ValueError):
+        opt.step(grads[:3] + [p[0].reshape(-1)[-1:]] + grads[4:])
+    opt.max_norm = 1.0
+    with pytest.raises(ValueError):
+        opt.step(grads)
+    assert opt.t == 0 and all(same_bits(a, b) for a, b in zip(before, p))
+    opt.max_norm = 0.0
+    # neighbours that only touch, and one gradient for two parameters, are fine
+    flat = torch.zeros(200, device="cuda")
+    g = torch.ones(100, device="cuda")
+    opt = zs.TensorOptimizer([flat[:100], flat[100:]], lr=1e-3, weight_decay=[0.1, 0.0])
+    opt.step([g, g])
+    assert opt.t == 1 and bool((flat < 0).all()) and same_bits(flat[:100], flat[100:])
