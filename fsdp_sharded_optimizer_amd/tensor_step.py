@@ -210,7 +210,9 @@ class CapturedTensorStep:
     def __init__(self, opt: TensorOptimizer, extra_norm_sq: float):
         if opt._grads is None:
             raise RuntimeError("capture() without bound gradients")
+        opt._check_clip()
         self.opt, self.extra_norm_sq = opt, extra_norm_sq
+        self._fixed = (opt.grad_scale, opt.compute_norm)   # in the recorded launches, not in device memory
         # what the graph reads and writes stays this object's, whatever is bound later
         self._grads, self._workspace = opt._grads, opt._workspace
         self._lists = [(decay, lst.clone()) for decay, _, lst in opt._groups]
@@ -221,27 +223,17 @@ class CapturedTensorStep:
         self._parts = self._dev.split(size)
         self._done = torch.cuda.Event()
         self._write(opt.t + 1)
-        # one warm-up run on a side stream, as capture requires; what it changes
-        # is saved first and restored after, so capturing changes nothing
-        saved = [(x, x.clone()) for x in self._live()]
+        # one warm-up run on a side stream, as capture requires, on a norm that is
+        # not finite: the step leaves everything as it is
         side = torch.cuda.Stream(device=dev)
         side.wait_stream(torch.cuda.current_stream(dev))
         with torch.cuda.stream(side):
-            self._body()
+            self._body(torch.full_like(opt.norm_sq, float("nan")))
         torch.cuda.current_stream(dev).wait_stream(side)
-        torch.cuda.synchronize(dev)
-        for to, src in saved:
-            to.copy_(src)
-        del saved
         torch.cuda.synchronize(dev)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
             self._body()
-
-    def _live(self) -> list:
-        """The tensors that a step writes."""
-        names = ("param", "param_bf16", "exp_avg", "exp_avg_sq", "state_q8")
-        return [x for _, lst in self._lists for name in names for x in lst.tensors.get(name) or [] if x is not None]
 
     def _bytes(self, k: int, t: int) -> bytes:
         hp = self.opt._hp(self._lists[k][0], self.extra_norm_sq, t)
@@ -252,11 +244,12 @@ class CapturedTensorStep:
         raw = b"".join(self._bytes(k, t) for k in range(len(self._lists)))
         self._host.numpy()[:] = np.frombuffer(raw, dtype=np.uint8)
 
-    def _body(self) -> None:
+    def _body(self, warm_up_norm: Optional[torch.Tensor] = None) -> None:
         opt = self.opt
         norm = None
         if opt.compute_norm:
             norm = zt.grad_norm_sq_tensors(self._grads, opt.grad_scale, opt.norm_sq, self._workspace)
+        norm = norm if warm_up_norm is None else warm_up_norm
         self._dev.copy_(self._host, non_blocking=True)
         for (_, lst), sc in zip(self._lists, self._parts):
             if opt.state_bits == 32:
@@ -266,7 +259,12 @@ class CapturedTensorStep:
 
     def replay(self) -> None:
         """Run the next step.  Waits for the previous replay to have read the
-        pinned scalars before rewriting them."""
+        pinned scalars before rewriting them.  lr, betas, eps and max_norm are
+        the optimizer's of now; grad_scale and compute_norm must be those of
+        the capture (the norm was recorded with them)."""
+        self.opt._check_clip()
+        if self._fixed != (self.opt.grad_scale, self.opt.compute_norm):
+            raise RuntimeError("replay(): grad_scale or compute_norm changed since the capture")
         self._done.synchronize()
         self._write(self.opt.t + 1)
         self.graph.replay()

@@ -263,3 +263,45 @@ def test_no_step_is_half_refused():
     opt = zs.TensorOptimizer([flat[:100], flat[100:]], lr=1e-3, weight_decay=[0.1, 0.0])
     opt.step([g, g])
     assert opt.t == 1 and bool((flat < 0).all()) and same_bits(flat[:100], flat[100:])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_follows_the_optimizer_or_refuses(bits):
+    """lr, betas and max_norm may change between replays; what is recorded in
+    the launches may not.  Capturing leaves every byte alone, also without a norm."""
+    kw = dict(KW, state_bits=bits)
+    params, twin = start(torch.float32), start(torch.float32)
+    opt, eager = zs.TensorOptimizer(params, **kw), zs.TensorOptimizer(twin, **kw)
+    grads = [g.clone() for g in gradients(3, torch.float32)]
+    opt.step(grads)
+    eager.step(grads)
+    before = [x.clone() for x in (opt._states if bits == 8 else opt._exp_avg + opt._exp_avg_sq)]
+    graph = opt.capture()
+    for a, b in zip(before, opt._states if bits == 8 else opt._exp_avg + opt._exp_avg_sq):
+        assert same_bits(a, b)
+    assert all(same_bits(a, b) for a, b in zip(params, twin))
+    for lr, betas, max_norm in ((1e-3, (0.9, 0.95), 1.0), (2e-3, (0.8, 0.99), 0.25), (5e-4, (0.9, 0.999), 0.0)):
+        for o in (opt, eager):
+            o.lr, o.betas, o.max_norm = lr, betas, max_norm
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+        assert all(same_bits(a, b) for a, b in zip(params, twin)), (lr, betas, max_norm)
+    t = opt.t
+    for name, value in (("grad_scale", 1.0), ("compute_norm", False)):
+        was = getattr(opt, name)
+        setattr(opt, name, value)
+        with pytest.raises(RuntimeError):
+            graph.replay()
+        setattr(opt, name, was)
+    graph.replay()
+    eager.step()
+    torch.cuda.synchronize()
+    assert opt.t == t + 1 and all(same_bits(a, b) for a, b in zip(params, twin))
+    plain = zs.TensorOptimizer(params, lr=1e-3, state_bits=bits)
+    plain.bind_grads(grads)
+    graph = plain.capture()
+    assert plain.t == 0 and all(same_bits(a, b) for a, b in zip(params, twin))
+    plain.max_norm = 1.0
+    with pytest.raises(ValueError):
+        graph.replay()
