@@ -31,7 +31,7 @@ struct Range {
 
 class Ranges {
 public:
-    static constexpr int kKinds = 6;
+    static constexpr int kKinds = 5;
     // room for `count` ranges of each kind; false: no memory
     bool reserve(int32_t count, int kinds) {
         per_ = (int64_t)count;
@@ -92,7 +92,7 @@ private:
     int64_t per_ = 0;
     int64_t count_[kKinds] = {};
     bool written_[kKinds] = {};
-    bool sorted_[kKinds] = {true, true, true, true, true, true};
+    bool sorted_[kKinds] = {true, true, true, true, true};
     Range extra_[2];
     int extras_ = 0;
 };

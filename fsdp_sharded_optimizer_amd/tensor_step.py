@@ -81,7 +81,7 @@ class TensorOptimizer:
             raise ValueError("weight_decay: finite values >= 0")
         if param_bf16 is not None and len(param_bf16) != len(params):
             raise ValueError(f"param_bf16: {len(param_bf16)} tensors for {len(params)}")
-        zt.GradTensors(params)   # the tensors' checks, before anything is allocated
+        checked = zt.GradTensors(params)   # the tensors' checks, before anything is allocated
         self.params, self.state_bits, self.seed = params, state_bits, zt._seed(seed, "TensorOptimizer")
         self.lr, self.betas, self.eps = lr, betas, eps
         self.grad_scale, self.max_norm = grad_scale, max_norm
@@ -107,7 +107,10 @@ class TensorOptimizer:
         self._grads: Optional[zt.GradTensors] = None
         dev = params[0].device
         self.norm_sq = torch.zeros(1, dtype=torch.float64, device=dev)
-        self._workspace = torch.empty(8, dtype=torch.uint8, device=dev)
+        # for gradients of either dtype: a run on another stream never sees it move
+        need = [zt._lib().grad_norm_sq_tensors_workspace_bytes(checked.address, checked.count, dtype)
+                for dtype in (zs.ZS_F32, zs.ZS_BF16)]
+        self._workspace = torch.empty(max(need + [8]), dtype=torch.uint8, device=dev)
         self.t = 0
 
     def bind_grads(self, grads: Sequence[torch.Tensor]) -> None:
@@ -124,9 +127,6 @@ class TensorOptimizer:
             raise ValueError("bind_grads: a gradient overlaps a parameter or a re-cast")
         for _, at, group in self._groups:
             group._take_grads(lst, at)
-        need = zt.grad_norm_sq_tensors_workspace_bytes(lst)
-        if need > self._workspace.numel():
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.norm_sq.device)
         self._grads = lst
 
     def _check_clip(self) -> None:
@@ -214,7 +214,7 @@ class CapturedTensorStep:
         self.opt, self.extra_norm_sq = opt, extra_norm_sq
         self._fixed = (opt.grad_scale, opt.compute_norm)   # in the recorded launches, not in device memory
         # what the graph reads and writes stays this object's, whatever is bound later
-        self._grads, self._workspace = opt._grads, opt._workspace
+        self._grads = opt._grads
         self._lists = [(decay, lst.clone()) for decay, _, lst in opt._groups]
         dev = opt.norm_sq.device
         size = len(self._bytes(0, 1))
@@ -248,7 +248,7 @@ class CapturedTensorStep:
         opt = self.opt
         norm = None
         if opt.compute_norm:
-            norm = zt.grad_norm_sq_tensors(self._grads, opt.grad_scale, opt.norm_sq, self._workspace)
+            norm = zt.grad_norm_sq_tensors(self._grads, opt.grad_scale, opt.norm_sq, opt._workspace)
         norm = norm if warm_up_norm is None else warm_up_norm
         self._dev.copy_(self._host, non_blocking=True)
         for (_, lst), sc in zip(self._lists, self._parts):

@@ -144,6 +144,7 @@ class GradTensors(_List):
     """Gradients (fp32 or bf16, one dtype) for grad_norm_sq_tensors."""
 
     def __init__(self, grads: Sequence[torch.Tensor]):
+        grads = list(grads)
         numels, device = _numels(grads, "grads")
         super().__init__(zs.Tensor, numels, device)
         self.set_grads(grads)
@@ -241,8 +242,9 @@ class Q8Moments(_List):
                 if t is None:
                     raise ValueError(f"tensor {k} has neither moment: give numels")
                 numels.append(t.numel())
+        pointers = _states(states, numels)
         super().__init__(MomentsQ8, numels, states[0].device if count else None)
-        self._set("state_q8", states, _states(states, self.numels))
+        self._set("state_q8", states, pointers)
         kinds = []
         for name, ts in zip(("exp_avg", "exp_avg_sq"), lists):
             pointers, kind = _pointers(ts, name, self.numels, _FLOATS, optional=True)
@@ -274,8 +276,10 @@ def grad_norm_sq_tensors(grads: Union[GradTensors, Sequence[torch.Tensor]], grad
     if out.dtype != torch.float64 or out.numel() < 1:
         raise TypeError("grad_norm_sq_tensors: out must hold one float64")
     if workspace is None:
-        workspace = torch.empty(max(grad_norm_sq_tensors_workspace_bytes(grads), 8), dtype=torch.uint8,
-                                device=out.device)
+        # of the stream it is used on: freed at return, it is next used in that stream's order
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(max(grad_norm_sq_tensors_workspace_bytes(grads), 8), dtype=torch.uint8,
+                                    device=out.device)
     zs._check("grad_norm_sq_tensors", _lib().grad_norm_sq_tensors(
         grads.address, grads.count, grads.grad_dtype, float(grad_scale), zs._dev(out, "out"),
         zs._dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), zs._stream(stream)))

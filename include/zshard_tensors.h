@@ -161,9 +161,13 @@ typedef struct {
  * adamw_step_tensors_q8 — adamw_step_tensors on 8-bit moments: each tensor's
  * moments are decoded, the new ones formed in fp32 as adamw_step forms them
  * (the same operations and roundings), the parameter updated with these, and
- * they are stored in 8 bits.  The key is mix(mix(seed) + step), step the low
+ * they are stored in 8 bits.  The parameter's step is formed with the
+ * hardware's root and reciprocal where eps >= 2^-40, within 8 * 2^-24 of the
+ * quotient of those moments.  The key is mix(mix(seed) + step), step the low
  * 32 bits of hp->step: the same call on the same data gives the same bits.
- * A non-finite norm leaves every tensor and its moments unchanged.
+ * A non-finite norm leaves every tensor and its moments unchanged; without a
+ * norm a gradient that is not finite makes its whole block's moments NaN.
+ * Full speed: param, and param_bf16, on a 128-byte boundary.
  */
 ZS_API int32_t adamw_step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_tensor* tensors,
                                      int32_t count, int32_t param_dtype, int32_t grad_dtype,

@@ -352,3 +352,26 @@ def test_offsets_past_32_bits():
     assert got_v.tolist() == [0.25 * (k + 1) ** 2 for k in range(len(spots))]
     assert (p[spots].cpu().float() - 1.5).abs().max() <= 2.0 ** -8 * 1.5
     assert int(torch.count_nonzero(m)) == len(spots) and int(torch.count_nonzero(p)) == len(spots)
+
+
+def test_the_norm_s_own_workspace_on_another_stream():
+    """Without a workspace the call takes one of the stream it runs on: memory
+    that is freed when it returns, while the kernels have yet to run, is not
+    handed to the current stream."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    grads = [torch.randn(300_000, generator=gen, device="cuda") for _ in range(4)]
+    lst = zs.GradTensors(grads)
+    need = zs.grad_norm_sq_tensors_workspace_bytes(lst)
+    want = zs.grad_norm_sq_tensors(lst, 1.0, torch.zeros(1, dtype=torch.float64, device="cuda"))
+    slow = torch.randn(4096, 4096, generator=gen, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = torch.zeros(1, dtype=torch.float64, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            slow @ slow
+    zs.grad_norm_sq_tensors(lst, 1.0, out, stream=side)
+    taken = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert same_bits(out, want) and all(bool((t == 255).all()) for t in taken)
