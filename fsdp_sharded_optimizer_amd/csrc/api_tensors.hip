@@ -174,6 +174,14 @@ int64_t line_shift(const zs_adamw_tensor& t, int64_t psz) {
     return off == 0 ? 0 : kListTile - (per - off);
 }
 
+// Whether b's elements come right after a's first n in every stream: the update
+// knows no tensors, so the two are one entry then (views of flat buffers: 25M
+// bf16 parameters in 290 tensors back to back, one launch instead of three).
+bool follows(const zs_adamw_tensor& a, int64_t n, const zs_adamw_tensor& b, int64_t psz, int64_t gsz) {
+    return b.param == advance(a.param, n * psz) && b.grad == advance(a.grad, n * gsz) && b.exp_avg == a.exp_avg + n &&
+           b.exp_avg_sq == a.exp_avg_sq + n && b.param_bf16 == advance(a.param_bf16, n * 2);
+}
+
 int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const zs_adamw_tensor* list, int32_t count,
                      int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev, void* hip_stream) {
     const int64_t total = list_total(list, count);
@@ -219,9 +227,13 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
     Filler<AdamwBatch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_tensor& t = list[k];
-        const int64_t shift = t.numel == 0 ? 0 : line_shift(t, psz);
-        for (int64_t off = 0; off < t.numel; off += kLaunchElems) {
-            const int64_t n = launch_piece(t.numel, off);
+        int64_t numel = t.numel;
+        if (numel == 0) continue;
+        while (k + 1 < count && (list[k + 1].numel == 0 || follows(t, numel, list[k + 1], psz, gsz)))
+            numel += list[++k].numel;
+        const int64_t shift = line_shift(t, psz);
+        for (int64_t off = 0; off < numel; off += kLaunchElems) {
+            const int64_t n = launch_piece(numel, off);
             int at = 0;
             const int32_t rc = fill.add(ceil_div(n + shift, kListTile), at);
             if (rc != ZS_OK) return rc;

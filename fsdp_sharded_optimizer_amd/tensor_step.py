@@ -29,10 +29,11 @@ from . import tensors as zt
 def _moments_like(params: Sequence[torch.Tensor]) -> list:
     """fp32 zeros for each tensor, views of one buffer.  Each starts at its
     parameter's element offset from a 128-byte boundary, so that the step can
-    put every stream it reads and writes on whole cache lines."""
+    put every stream it reads and writes on whole cache lines; those of
+    parameters that follow one another do so too."""
     spots, at = [], 0
     for p in params:
-        at = -(-at // 32) * 32 + p.data_ptr() % 128 // p.element_size() % 32
+        at += (p.data_ptr() % 128 // p.element_size() - at) % 32
         spots.append(at)
         at += p.numel()
     buffer = torch.zeros(max(at, 1), dtype=torch.float32, device=params[0].device)

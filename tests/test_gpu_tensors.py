@@ -375,3 +375,31 @@ def test_the_norm_s_own_workspace_on_another_stream():
     taken = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert same_bits(out, want) and all(bool((t == 255).all()) for t in taken)
+
+
+@pytest.mark.parametrize("broken", [None, "p", "g", "m", "v", "c", "missing", "order"])
+def test_tensors_that_follow_one_another(broken):
+    """Views of flat buffers, where neighbours may be taken as one, and lists in
+    which one stream is not like that: moved at one tensor, without a re-cast,
+    or with the tensors in another order."""
+    numels = [300, 1, 0, 255, 1024, 77, 0, 513, 31]
+    pools, *_ = a_list(numels, torch.float32, torch.bfloat16, True, 1)
+    if broken in pools:     # the fifth tensor's is elsewhere
+        x = pools[broken].views[4]
+        pools[broken].views[4] = x.clone()
+    copies = list(pools["c"].views)
+    if broken == "missing":
+        copies[3] = copies[4] = None
+    order = list(range(len(numels)))
+    if broken == "order":
+        order = [1, 0, 2, 4, 3, 5, 8, 7, 6]
+    hp = zs.AdamWConfig(**HP, step=3)
+    want = one_by_one(pools, hp, None)
+    pick = lambda ts: [ts[k] for k in order]  # noqa: E731
+    left = [c.clone() for c in pools["c"].views]
+    zs.adamw_step_tensors(hp, zs.AdamWTensors(pick(pools["p"].views), pick(pools["g"].views), pick(pools["m"].views),
+                                              pick(pools["v"].views), pick(copies)))
+    for k, w in enumerate(want):
+        for n in ("p", "m", "v"):
+            assert same_bits(pools[n].views[k], w[n]), (k, n)
+        assert same_bits(pools["c"].views[k], w["c"] if copies[k] is not None else left[k]), k
