@@ -30,7 +30,7 @@ template <bool PBF16, bool GBF16>
 constexpr unsigned kLds = PBF16 ? (GBF16 ? 10240 : 12288) : (GBF16 ? 13312 : 14336);
 constexpr int64_t kCapTiles = 32768;
 
-template <bool PBF16, bool GBF16, bool DEV>
+template <bool PBF16, bool GBF16, bool DEV, bool KEEP>
 __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b) {
     using P = typename GradType<PBF16>::T;
     using G = typename GradType<GBF16>::T;
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b
     float coef;
     if (i >= 0 && i + 4 <= n) {
         // the loads are issued before the clip coefficient is resolved
-        const f32x4 g4 = ld4(grad + i);
+        const f32x4 g4 = ld4<KEEP>(grad + i);
         f32x4 p4 = ld4(param + i);
         f32x4 m4 = ld4(exp_avg + i);
         f32x4 v4 = ld4(exp_avg_sq + i);
@@ -85,22 +85,24 @@ __global__ __launch_bounds__(kWave) void adamw_tensors_kernel(const AdamwBatch b
 }
 
 template <bool PBF16, bool GBF16>
-hipError_t launch(const AdamwBatch& b, int64_t tiles, hipStream_t stream) {
+hipError_t launch(const AdamwBatch& b, bool keep, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     const unsigned lds = tiles < kCapTiles ? 0 : kLds<PBF16, GBF16>;
-    if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, true>), grid, block, lds, stream, b);
-    else
-        hipLaunchKernelGGL((adamw_tensors_kernel<PBF16, GBF16, false>), grid, block, lds, stream, b);
+    const auto kernel =
+        b.sc_dev != nullptr
+            ? (keep ? adamw_tensors_kernel<PBF16, GBF16, true, true> : adamw_tensors_kernel<PBF16, GBF16, true, false>)
+            : (keep ? adamw_tensors_kernel<PBF16, GBF16, false, true> : adamw_tensors_kernel<PBF16, GBF16, false, false>);
+    hipLaunchKernelGGL(kernel, grid, block, lds, stream, b);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, int64_t tiles,
+hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
                                 hipStream_t stream) {
-    if (param_bf16) return grad_bf16 ? launch<true, true>(b, tiles, stream) : launch<true, false>(b, tiles, stream);
-    return grad_bf16 ? launch<false, true>(b, tiles, stream) : launch<false, false>(b, tiles, stream);
+    if (param_bf16)
+        return grad_bf16 ? launch<true, true>(b, keep, tiles, stream) : launch<true, false>(b, keep, tiles, stream);
+    return grad_bf16 ? launch<false, true>(b, keep, tiles, stream) : launch<false, false>(b, keep, tiles, stream);
 }
 
 }  // namespace zs

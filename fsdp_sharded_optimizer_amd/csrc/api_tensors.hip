@@ -219,10 +219,12 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
     AdamwBatch b;
     std::memset(&b, 0, sizeof(b));
     if (sc_dev == nullptr) b.sc = make_scalars(hp);
+    const bool keep = keep_grads(total * gsz);
     b.sc_dev = reinterpret_cast<const AdamwScalars*>(sc_dev);
     b.norm_sq = norm_sq_dev;
     auto launch = [&](const AdamwBatch& x, int64_t tiles) {
-        return launch_adamw_tensors(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, tiles, as_stream(hip_stream));
+        return launch_adamw_tensors(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, keep, tiles,
+                                    as_stream(hip_stream));
     };
     Filler<AdamwBatch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
@@ -274,14 +276,15 @@ int32_t add_q8(Q8Batch& batch, Fill& fill, int64_t tile, void* state, int64_t nu
     return ZS_OK;
 }
 
-// Counts the elements whose written streams start off a cache line: tiles are
-// taken in runs where they are most of a list.
+// Counts the elements whose streams start off a cache line: where they are most
+// of a list, tiles are taken in runs, and what is read of these streams is kept
+// for the neighbour that shares a line.
 struct OffLine {
     int64_t elems = 0;
     void add(int64_t numel, const void* a, const void* b) {
         if (!aligned(a, kLine) || !aligned(b, kLine)) elems += numel;
     }
-    uint32_t runs(int64_t total) const { return elems > total / 2 ? 1 : 0; }
+    uint32_t most_of(int64_t total) const { return elems > total / 2 ? 1 : 0; }
 };
 
 int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_scalars* sc_dev,
@@ -323,11 +326,12 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         b.sc.adamw = make_scalars(hp);
         b.sc.key = q8_key(seed, hp->step);
     }
-    b.runs = off_line.runs(total);
+    b.runs = off_line.most_of(total);
+    const bool keep = keep_grads(total * gsz);
     b.sc_dev = reinterpret_cast<const Q8Scalars*>(sc_dev);
     b.norm_sq = norm_sq_dev;
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
-        return launch_adamw_q8(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, tiles, as_stream(hip_stream));
+        return launch_adamw_q8(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, keep, tiles, as_stream(hip_stream));
     };
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
@@ -356,15 +360,15 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
         ranges.add(0, t.exp_avg, t.numel * sz, !encode);
         ranges.add(1, t.exp_avg_sq, t.numel * sz, !encode);
         ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), encode);
-        if (!encode) off_line.add(t.numel, t.exp_avg, t.exp_avg_sq);
+        off_line.add(t.numel, t.exp_avg, t.exp_avg_sq);
     }
     if (ranges.clash()) return ZS_EOVERLAP;
     Q8Batch b;
     std::memset(&b, 0, sizeof(b));
-    b.runs = off_line.runs(total);
+    b.runs = off_line.most_of(total);   // (of a storing one: whether it keeps what it reads)
     b.sc.key = q8_key(seed, 0);
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
-        return encode ? launch_q8_encode(x, dtype == ZS_BF16, tile, tiles, as_stream(hip_stream))
+        return encode ? launch_q8_encode(x, dtype == ZS_BF16, x.runs != 0, tile, tiles, as_stream(hip_stream))
                       : launch_q8_decode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream));
     };
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
@@ -420,9 +424,10 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
     int64_t done = 0;   // partials of the launches before
     NormBatch b;
     std::memset(&b, 0, sizeof(b));
+    const bool keep = keep_grads(list_total(grads, count) * gsz);
     auto launch = [&](const NormBatch& x, int64_t tiles) {
         // a list of one tile: its partial is the result
-        const hipError_t e = launch_norm_tensors(x, grad_dtype == ZS_BF16, tiles, (float)grad_scale,
+        const hipError_t e = launch_norm_tensors(x, grad_dtype == ZS_BF16, keep, tiles, (float)grad_scale,
                                                  parts == 1 ? out_sq_dev : partials + done, as_stream(hip_stream));
         done += tiles;
         return e;

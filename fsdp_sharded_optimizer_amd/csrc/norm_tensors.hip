@@ -23,7 +23,7 @@ constexpr unsigned kLds = 24576;
 template <bool BF16> constexpr int kVec = BF16 ? 8 : 4;   // elements of a 128-bit load
 template <bool BF16> constexpr int64_t kTile = (int64_t)kBlock * kVec<BF16> * kQ;
 
-template <bool BF16>
+template <bool BF16, bool KEEP>
 __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b, float scale,
                                                               double* __restrict__ partials) {
     constexpr int VE = kVec<BF16>;
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     if (tile + kTile<BF16> <= n) {
         u32x4 v[kQ];
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) v[q] = ld_stream_u32x4_any(grad + lane0 + q * kBlock * VE);
+        for (int q = 0; q < kQ; ++q) v[q] = ld_u32x4_any<KEEP>(grad + lane0 + q * kBlock * VE);
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
             if constexpr (BF16) {
@@ -74,12 +74,18 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
 
 int64_t norm_tile_elems(int grad_bf16) { return grad_bf16 ? kTile<true> : kTile<false>; }
 
-hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, int64_t tiles, float scale, double* partials,
-                               hipStream_t stream) {
-    static_assert(kLaunchElems % kTile<true> == 0, "pieces of a tensor keep its tiles");
+template <bool BF16>
+static void launch(const NormBatch& b, bool keep, int64_t tiles, float scale, double* partials, hipStream_t stream) {
+    static_assert(kLaunchElems % kTile<BF16> == 0, "pieces of a tensor keep its tiles");
     const dim3 grid((unsigned)tiles), block(kBlock);
-    if (grad_bf16) hipLaunchKernelGGL(norm_tensors_kernel<true>, grid, block, kLds, stream, b, scale, partials);
-    else hipLaunchKernelGGL(norm_tensors_kernel<false>, grid, block, kLds, stream, b, scale, partials);
+    if (keep) hipLaunchKernelGGL((norm_tensors_kernel<BF16, true>), grid, block, kLds, stream, b, scale, partials);
+    else hipLaunchKernelGGL((norm_tensors_kernel<BF16, false>), grid, block, kLds, stream, b, scale, partials);
+}
+
+hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, bool keep, int64_t tiles, float scale,
+                               double* partials, hipStream_t stream) {
+    if (grad_bf16) launch<true>(b, keep, tiles, scale, partials, stream);
+    else launch<false>(b, keep, tiles, scale, partials, stream);
     return hipGetLastError();
 }
 

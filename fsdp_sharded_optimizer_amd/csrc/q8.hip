@@ -44,8 +44,8 @@ struct Chunk {
     uint8_t* scales;   // the first chunk's
 };
 template <int CHUNKS>
-__device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
-    const uint32_t w = b.runs ? tile_in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
+__device__ __forceinline__ Chunk chunk_of(const Q8Batch& b, bool runs) {
+    const uint32_t w = runs ? tile_in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     uint32_t first_tile;
     const Q8Entry e = b.e[find_tensor(b.tab, w, first_tile)];
     const Q8At at = q8_at(e);
@@ -55,10 +55,10 @@ __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b) {
 }
 
 // 4 consecutive elements from i of n (zeros past the end).
-template <typename T>
+template <bool KEEP, typename T>
 __device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool whole, float (&x)[4]) {
     if (whole || i + 4 <= n) {
-        const f32x4 w = ld4(p + i);
+        const f32x4 w = ld4<KEEP>(p + i);
         x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
     } else {
 #pragma unroll
@@ -157,8 +157,12 @@ __device__ __forceinline__ float adam_ratio(const AdamwScalars& a, float inv_roo
 }
 constexpr float kFastEps = 0x1p-40f;
 
-// One chunk's step.  WHOLE: all its elements are the tensor's.
-template <bool PBF16, bool GBF16, bool WHOLE, bool FAST>
+// One chunk's step.  WHOLE: all its elements are the tensor's.  KEEP: of the
+// gradients (keep_grads).  RUNS: the written streams lie off cache lines, tiles are
+// taken in runs, and a parameter line that two tiles share is kept in their L2
+// (405M fp32 parameters at odd offsets 1210 -> 1184 us, bf16 727 -> 714; on aligned
+// tensors 1-4 % slower).
+template <bool PBF16, bool GBF16, bool WHOLE, bool FAST, bool KEEP, bool RUNS>
 __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc, const Chunk& c) {
     using P = typename GradType<PBF16>::T;
     using G = typename GradType<GBF16>::T;
@@ -169,12 +173,12 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
     float g[kBlocks][4], p[kBlocks][4], m[kBlocks][4], v[kBlocks][4];
     uint32_t mc[kBlocks], vc[kBlocks];
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) load4(grad, c.i + k * kQ8Block, n, WHOLE, g[k]);
+    for (int k = 0; k < kBlocks; ++k) load4<KEEP>(grad, c.i + k * kQ8Block, n, WHOLE, g[k]);
     load_codes(c.codes, mc);
     load_codes(c.codes + kQ8Pad, vc);
     uint32_t scales = load_scales(c.scales);
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) load4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
+    for (int k = 0; k < kBlocks; ++k) load4<RUNS>(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
     float coef;
     if (!clip_coef(sc.adamw, b.norm_sq, coef)) return;
     scales = uniform(scales);
@@ -217,19 +221,21 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
     store_moments<1>(c, sc.key, m, v);
 }
 
-template <bool PBF16, bool GBF16, bool DEV>
+template <bool PBF16, bool GBF16, bool DEV, bool KEEP, bool RUNS>
 __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
-    const Chunk c = chunk_of<1>(b);
+    const Chunk c = chunk_of<1>(b, RUNS);
     const Q8Scalars sc = DEV ? *b.sc_dev : b.sc;
-    if (c.first + kQ8Pad <= (int64_t)c.e.numel && sc.adamw.eps >= kFastEps) step_chunk<PBF16, GBF16, true, true>(b, sc, c);
-    else step_chunk<PBF16, GBF16, false, false>(b, sc, c);
+    if (c.first + kQ8Pad <= (int64_t)c.e.numel && sc.adamw.eps >= kFastEps)
+        step_chunk<PBF16, GBF16, true, true, KEEP, RUNS>(b, sc, c);
+    else
+        step_chunk<PBF16, GBF16, false, false, KEEP, RUNS>(b, sc, c);
 }
 
-template <bool BF16, int CHUNKS>
+template <bool BF16, int CHUNKS, bool KEEP>
 __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
     constexpr int kAll = CHUNKS * kBlocks;
-    const Chunk c = chunk_of<CHUNKS>(b);
+    const Chunk c = chunk_of<CHUNKS>(b, false);
     const int64_t n = c.e.numel;
     const bool whole = c.first + CHUNKS * kQ8Pad <= n;
     const T* const from_m = unpack_ptr<const T>(c.e.lo[0], c.e.hi[0]);
@@ -238,8 +244,8 @@ __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
 #pragma unroll
     for (int k = 0; k < kAll; ++k) {
         const int64_t i = c.i + k * kQ8Block;
-        if (from_m != nullptr) load4(from_m, i, n, whole, m[k]);
-        if (from_v != nullptr) load4(from_v, i, n, whole, v[k]);
+        if (from_m != nullptr) load4<KEEP>(from_m, i, n, whole, m[k]);
+        if (from_v != nullptr) load4<KEEP>(from_v, i, n, whole, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < kAll; ++k)
@@ -251,7 +257,7 @@ __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
 template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
-    const Chunk c = chunk_of<1>(b);
+    const Chunk c = chunk_of<1>(b, b.runs != 0);
     const int64_t n = c.e.numel;
     const bool whole = c.first + kQ8Pad <= n;
     uint32_t mc[kBlocks], vc[kBlocks];
@@ -276,30 +282,41 @@ __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     }
 }
 
-template <bool PBF16, bool GBF16>
+template <bool PBF16, bool GBF16, bool KEEP, bool RUNS>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
     const unsigned lds = cap(kStepLds<PBF16>, tiles * kQ8Pad);
     if (b.sc_dev != nullptr)
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true>), grid, block, lds, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true, KEEP, RUNS>), grid, block, lds, stream, b);
     else
-        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false>), grid, block, lds, stream, b);
+        hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, false, KEEP, RUNS>), grid, block, lds, stream, b);
     return hipGetLastError();
+}
+template <bool PBF16, bool GBF16>
+hipError_t launch_step(const Q8Batch& b, bool keep, int64_t tiles, hipStream_t stream) {
+    if (keep)
+        return b.runs ? launch_step<PBF16, GBF16, true, true>(b, tiles, stream)
+                      : launch_step<PBF16, GBF16, true, false>(b, tiles, stream);
+    return b.runs ? launch_step<PBF16, GBF16, false, true>(b, tiles, stream)
+                  : launch_step<PBF16, GBF16, false, false>(b, tiles, stream);
 }
 
 }  // namespace
 
-hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream) {
+hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
+                           hipStream_t stream) {
     if (param_bf16)
-        return grad_bf16 ? launch_step<true, true>(b, tiles, stream) : launch_step<true, false>(b, tiles, stream);
-    return grad_bf16 ? launch_step<false, true>(b, tiles, stream) : launch_step<false, false>(b, tiles, stream);
+        return grad_bf16 ? launch_step<true, true>(b, keep, tiles, stream)
+                         : launch_step<true, false>(b, keep, tiles, stream);
+    return grad_bf16 ? launch_step<false, true>(b, keep, tiles, stream)
+                     : launch_step<false, false>(b, keep, tiles, stream);
 }
 
-template <bool BF16>
+template <bool BF16, bool KEEP>
 static hipError_t encode(const Q8Batch& b, int64_t tile, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (tile == kQ8Pad) hipLaunchKernelGGL((q8_encode_kernel<BF16, 1>), grid, block, 0, stream, b);
-    else hipLaunchKernelGGL((q8_encode_kernel<BF16, 2>), grid, block, kEncodeLds, stream, b);
+    if (tile == kQ8Pad) hipLaunchKernelGGL((q8_encode_kernel<BF16, 1, KEEP>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((q8_encode_kernel<BF16, 2, KEEP>), grid, block, kEncodeLds, stream, b);
     return hipGetLastError();
 }
 
@@ -307,8 +324,10 @@ static hipError_t encode(const Q8Batch& b, int64_t tile, int64_t tiles, hipStrea
 // (one is as fast up to 34M elements, and faster below 4M).
 int64_t q8_encode_tile(int64_t total) { return total < kCapElems ? kQ8Pad : 2 * kQ8Pad; }
 
-hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t tiles, hipStream_t stream) {
-    return bf16 ? encode<true>(b, tile, tiles, stream) : encode<false>(b, tile, tiles, stream);
+// keep: 405M moments at odd offsets 714 -> 691 us (bf16 731 -> 703); aligned 648 -> 686
+hipError_t launch_q8_encode(const Q8Batch& b, int bf16, bool keep, int64_t tile, int64_t tiles, hipStream_t stream) {
+    if (bf16) return keep ? encode<true, true>(b, tile, tiles, stream) : encode<true, false>(b, tile, tiles, stream);
+    return keep ? encode<false, true>(b, tile, tiles, stream) : encode<false, false>(b, tile, tiles, stream);
 }
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {

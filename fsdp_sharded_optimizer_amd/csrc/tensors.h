@@ -82,23 +82,35 @@ inline uint32_t ptr_hi(const void* p) { return (uint32_t)(reinterpret_cast<uintp
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-__device__ __forceinline__ u32x4 ld_stream_u32x4_any(const void* p) {
-    return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
-}
-__device__ __forceinline__ u32x2 ld_stream_u32x2_any(const void* p) {
-    return __builtin_nontemporal_load(static_cast<const u32x2_any*>(p));
-}
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
 template <bool BF16> struct GradType { using T = float; };
 template <> struct GradType<true> { using T = uint16_t; };
 
-// Four consecutive elements of an fp32 or bf16 stream, as fp32.
+// Four consecutive elements of an fp32 or bf16 stream, as fp32.  KEEP: read so
+// that the caches keep the lines, instead of as a stream (a template argument:
+// of two branches that differ in this alone the compiler makes one load).
+template <bool KEEP = false>
 __device__ __forceinline__ f32x4 ld4(const float* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(p));
+    const f32x4_any* const q = reinterpret_cast<const f32x4_any*>(p);
+    if constexpr (KEEP) return *q;
+    else return __builtin_nontemporal_load(q);
 }
+template <bool KEEP>
+__device__ __forceinline__ u32x2 ld_u32x2_any(const void* p) {
+    const u32x2_any* const q = static_cast<const u32x2_any*>(p);
+    if constexpr (KEEP) return *q;
+    else return __builtin_nontemporal_load(q);
+}
+template <bool KEEP>
+__device__ __forceinline__ u32x4 ld_u32x4_any(const void* p) {
+    const u32x4_any* const q = static_cast<const u32x4_any*>(p);
+    if constexpr (KEEP) return *q;
+    else return __builtin_nontemporal_load(q);
+}
+template <bool KEEP = false>
 __device__ __forceinline__ f32x4 ld4(const uint16_t* p) {
-    const u32x2 w = ld_stream_u32x2_any(p);
+    const u32x2 w = ld_u32x2_any<KEEP>(p);
     return f32x4{bf16_to_f32(w.x & 0xFFFFu), bf16_to_f32(w.x >> 16), bf16_to_f32(w.y & 0xFFFFu),
                  bf16_to_f32(w.y >> 16)};
 }
@@ -118,6 +130,15 @@ constexpr int64_t kListMaxTiles = (int64_t(1) << 32) / 256 - 1;   // so starts f
 // A tensor of more than kLaunchElems elements is cut into entries of that many
 // (a multiple of every tile), so an entry's numel fits 32 bits.
 
+// Whether a list's gradients are read so that the last-level cache (256 MiB)
+// keeps them: they fit it, the norm reads them before the step does, and a
+// backward pass wrote the last of them shortly before that.  The other streams go
+// past it.  Norm and step of bf16 gradients as streams / kept, us: 34M parameters
+// 132 / 124, 76M 279 / 261, 124M 454 / 423 (fp32 ones with re-casts 164 / 159, 354 /
+// 338, 564 / 543; 8-bit moments 153 / 148 at 76M), 148M the same, 190M 690 / 696.
+constexpr int64_t kKeepBytes = int64_t(240) << 20;
+inline bool keep_grads(int64_t grad_bytes) { return grad_bytes <= kKeepBytes; }
+
 // --- the squared norm -----------------------------------------------------
 struct NormEntry {
     uint32_t lo, hi, numel;
@@ -128,8 +149,8 @@ struct NormBatch {
 };
 static_assert(sizeof(NormBatch) <= 4072, "kernel arguments");
 int64_t norm_tile_elems(int grad_bf16);   // elements per workgroup (one binary64 partial each)
-hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, int64_t tiles, float scale, double* partials,
-                               hipStream_t stream);
+hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, bool keep, int64_t tiles, float scale,
+                               double* partials, hipStream_t stream);
 
 // --- AdamW, fp32 moments --------------------------------------------------
 // Tile 0 of a tensor starts `shift` elements before its first one, so that the
@@ -149,7 +170,7 @@ struct AdamwBatch {
 };
 constexpr int64_t kListTile = 256;
 static_assert(sizeof(AdamwBatch) <= 4096, "kernel arguments");
-hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, int64_t tiles,
+hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
                                 hipStream_t stream);
 
 // --- 8-bit moments --------------------------------------------------------
@@ -191,8 +212,10 @@ static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
 // elements per workgroup of the storing conversion, for a list of that many in
 // all (the step and the reading one: kQ8Pad)
 int64_t q8_encode_tile(int64_t total);
-hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, int64_t tiles, hipStream_t stream);
-hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tile, int64_t tiles, hipStream_t stream);
+hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
+                           hipStream_t stream);
+// keep: the moments lie off cache lines
+hipError_t launch_q8_encode(const Q8Batch& b, int bf16, bool keep, int64_t tile, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
 
 }  // namespace zs
