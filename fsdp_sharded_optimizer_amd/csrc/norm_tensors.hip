@@ -23,6 +23,21 @@ constexpr unsigned kLds = 24576;
 template <bool BF16> constexpr int kVec = BF16 ? 8 : 4;   // elements of a 128-bit load
 template <bool BF16> constexpr int64_t kTile = (int64_t)kBlock * kVec<BF16> * kQ;
 
+// the elements from `at` of n that a 128-bit load would bring, zeros past the end
+template <bool BF16>
+__device__ __forceinline__ u32x4 last_words(const typename GradType<BF16>::T* grad, int64_t at, int64_t n) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16)
+            w[j] = (at + 2 * j < n ? (uint32_t)grad[at + 2 * j] : 0u) |
+                   (at + 2 * j + 1 < n ? (uint32_t)grad[at + 2 * j + 1] << 16 : 0u);
+        else
+            w[j] = at + j < n ? __float_as_uint(grad[at + j]) : 0u;
+    }
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 template <bool BF16, bool KEEP>
 __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b, float scale,
                                                               double* __restrict__ partials) {
@@ -34,37 +49,33 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     const int64_t n = e.numel;
     const int64_t tile = (int64_t)(blockIdx.x - first) * kTile<BF16>;
     const int64_t lane0 = tile + threadIdx.x * VE;
-    double s0 = 0.0, s1 = 0.0;
+    u32x4 v[kQ];
     if (tile + kTile<BF16> <= n) {
-        u32x4 v[kQ];
 #pragma unroll
         for (int q = 0; q < kQ; ++q) v[q] = ld_u32x4_any<KEEP>(grad + lane0 + q * kBlock * VE);
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-            if constexpr (BF16) {
-                const float lo[4] = {bf16_to_f32(v[q].x & 0xFFFFu), bf16_to_f32(v[q].x >> 16),
-                                     bf16_to_f32(v[q].y & 0xFFFFu), bf16_to_f32(v[q].y >> 16)};
-                const float hi[4] = {bf16_to_f32(v[q].z & 0xFFFFu), bf16_to_f32(v[q].z >> 16),
-                                     bf16_to_f32(v[q].w & 0xFFFFu), bf16_to_f32(v[q].w >> 16)};
-                add_squares4(lo, scale, s0, s1);
-                add_squares4(hi, scale, s0, s1);
-            } else {
-                const float g[4] = {__uint_as_float(v[q].x), __uint_as_float(v[q].y), __uint_as_float(v[q].z),
-                                    __uint_as_float(v[q].w)};
-                add_squares4(g, scale, s0, s1);
-            }
-        }
     } else {   // a tensor's ragged last tile: elements past the end add +0
 #pragma unroll
-        for (int q = 0; q < kQ; ++q)
+        for (int q = 0; q < kQ; ++q) {
+            const int64_t at = lane0 + q * kBlock * VE;
+            if (at + VE <= n) v[q] = ld_u32x4_any<KEEP>(grad + at);
+            else v[q] = last_words<BF16>(grad, at, n);
+        }
+    }
+    double s0 = 0.0, s1 = 0.0;
 #pragma unroll
-            for (int h = 0; h < VE; h += 4) {
-                const int64_t at = lane0 + q * kBlock * VE + h;
-                float g[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) g[j] = at + j < n ? widen(grad[at + j]) : 0.0f;
-                add_squares4(g, scale, s0, s1);
-            }
+    for (int q = 0; q < kQ; ++q) {
+        if constexpr (BF16) {
+            const float lo[4] = {bf16_to_f32(v[q].x & 0xFFFFu), bf16_to_f32(v[q].x >> 16),
+                                 bf16_to_f32(v[q].y & 0xFFFFu), bf16_to_f32(v[q].y >> 16)};
+            const float hi[4] = {bf16_to_f32(v[q].z & 0xFFFFu), bf16_to_f32(v[q].z >> 16),
+                                 bf16_to_f32(v[q].w & 0xFFFFu), bf16_to_f32(v[q].w >> 16)};
+            add_squares4(lo, scale, s0, s1);
+            add_squares4(hi, scale, s0, s1);
+        } else {
+            const float g[4] = {__uint_as_float(v[q].x), __uint_as_float(v[q].y), __uint_as_float(v[q].z),
+                                __uint_as_float(v[q].w)};
+            add_squares4(g, scale, s0, s1);
+        }
     }
     const double total = block_sum(s0 + s1);
     if (threadIdx.x == 0) partials[xcd_slot(blockIdx.x, gridDim.x)] = total;
