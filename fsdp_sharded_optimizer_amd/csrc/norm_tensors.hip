@@ -50,7 +50,25 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     const int64_t tile = (int64_t)(blockIdx.x - first) * kTile<BF16>;
     const int64_t lane0 = tile + threadIdx.x * VE;
     u32x4 v[kQ];
-    if (tile + kTile<BF16> <= n) {
+    if (BF16 && (e.lo & 2) && tile + kTile<BF16> < n) {
+        // bf16 at an odd offset: a lane's 16 bytes would span 5 words.  The words
+        // from its second element on instead; its first element is in the last
+        // word of the lane before (of a wave's first lane: loaded by itself).
+        uint32_t head[kQ] = {};
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) v[q] = ld_u32x4_any<KEEP>(grad + lane0 + q * kBlock * VE + 1);
+        if (threadIdx.x % 64 == 0) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) head[q] = (uint32_t)grad[lane0 + q * kBlock * VE] << 16;
+        }
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            const u32x4 w = v[q];
+            const uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp((int)head[q], (int)w.w, 0x138, 0xF, 0xF, false);   // wave_shr:1
+            v[q] = u32x4{__builtin_amdgcn_alignbit(w.x, before, 16), __builtin_amdgcn_alignbit(w.y, w.x, 16),
+                         __builtin_amdgcn_alignbit(w.z, w.y, 16), __builtin_amdgcn_alignbit(w.w, w.z, 16)};
+        }
+    } else if (tile + kTile<BF16> <= n) {
 #pragma unroll
         for (int q = 0; q < kQ; ++q) v[q] = ld_u32x4_any<KEEP>(grad + lane0 + q * kBlock * VE);
     } else {   // a tensor's ragged last tile: elements past the end add +0
