@@ -13,7 +13,7 @@ import torch
 import fsdp_sharded_optimizer_amd as zs
 from tests import tensors_reference as ref
 from tests.parity import from_np, to_np
-from tests.test_gpu_tensors import HP, LISTS, Pool, draws, same_bits
+from tests.test_gpu_tensors import HP, LISTS, Pool, at_offset, draws, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -327,3 +327,24 @@ def test_a_tensor_past_2_31_elements():
         assert equal_values(m[start:hi], ref.decode(*ref.encode(nm, "m", word), "m")), lo
         assert equal_values(v[start:hi], ref.decode(*ref.encode(nv, "v", word), "v")), lo
     assert int(torch.count_nonzero(v)) == sum(int((x != 0).sum()) for x in rows[:2]) + int(np.count_nonzero(rows[2]))
+
+
+@pytest.mark.parametrize("pdtype", [torch.float32, torch.bfloat16])
+def test_long_lists_off_cache_lines(pdtype):
+    """More gradients than the last-level cache holds, as one tensor at odd
+    offsets: stored, stepped and read out as the same tensor on 512-byte
+    boundaries."""
+    n = 130_000_003
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    p, m, v, g = (torch.randn(n, generator=gen, device="cuda") * s for s in (0.05, 1e-3, 1e-3, 0.1))
+    p, v, g = p.to(pdtype), v * v, g.bfloat16()
+    done = []
+    for off in (0, 1):
+        ps, gs, ms, vs = (at_offset(x, off) for x in (p, g, m, v))
+        state = torch.zeros(zs.moments_q8_bytes(n), dtype=torch.uint8, device="cuda")
+        zs.moments_q8_encode(zs.Q8Moments([state], [ms], [vs]), seed=6)
+        zs.adamw_step_tensors_q8(zs.AdamWConfig(**HP, step=4), zs.AdamWQ8Tensors([ps], [gs], [state]), seed=2)
+        zs.moments_q8_decode(zs.Q8Moments([state], [ms], [vs]))
+        done.append((state, ps, ms, vs))
+    for a, b in zip(*done):
+        assert torch.equal(a, b)

@@ -403,3 +403,45 @@ def test_tensors_that_follow_one_another(broken):
         for n in ("p", "m", "v"):
             assert same_bits(pools[n].views[k], w[n]), (k, n)
         assert same_bits(pools["c"].views[k], w["c"] if copies[k] is not None else left[k]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_around_a_tile_at_every_offset(dtype):
+    """Lengths around the ends of tiles, at offsets of 0 to 8 elements, between
+    values that are not numbers: the bits of the same tensor by itself."""
+    for n in (1, 7, 8, 511, 512, 513, 4095, 4096, 4097, 8191, 8192, 8193, 16384, 16391, 24577):
+        x = torch.from_numpy(draws([n], n, 1.0, dtype == torch.bfloat16)[0]).to("cuda", dtype)
+        want = zs.grad_norm_sq_tensors([x], 0.3, torch.zeros(1, dtype=torch.float64, device="cuda"))
+        for off in range(9):
+            buffer = torch.full((n + 80,), math.nan, dtype=dtype, device="cuda")
+            view = buffer[32 + off:32 + off + n]
+            view.copy_(x)
+            out = zs.grad_norm_sq_tensors([view], 0.3, torch.zeros(1, dtype=torch.float64, device="cuda"))
+            assert same_bits(out, want), (n, off)
+
+
+def at_offset(x, off):
+    """A copy of x that starts `off` elements into a buffer."""
+    buffer = torch.zeros(x.numel() + 64, dtype=x.dtype, device="cuda")
+    buffer[off:off + x.numel()] = x
+    return buffer[off:off + x.numel()]
+
+
+@pytest.mark.parametrize("gdtype,n", [(torch.bfloat16, 130_000_003), (torch.float32, 65_000_001)])
+def test_long_gradients_at_any_offset(gdtype, n):
+    """More gradients than the last-level cache holds: norm and step of views
+    at odd offsets against the same list on 512-byte boundaries."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    p, m, v, g = (torch.randn(n, generator=gen, device="cuda") * s for s in (0.05, 1e-3, 1e-3, 0.1))
+    v, g = v * v, g.to(gdtype)
+    hp = zs.AdamWConfig(**HP, max_norm=1.0, step=4)
+    done = []
+    for offs in ((0, 0, 0, 0, 0), (1, 1, 1, 1, 1), (0, 3, 1, 2, 5)):
+        ps, gs, ms, vs = (at_offset(x, o) for x, o in zip((p, g, m, v), offs))
+        c = at_offset(torch.zeros(n, dtype=torch.bfloat16, device="cuda"), offs[4])
+        norm = zs.grad_norm_sq_tensors([gs], hp.grad_scale, torch.zeros(1, dtype=torch.float64, device="cuda"))
+        zs.adamw_step_tensors(hp, zs.AdamWTensors([ps], [gs], [ms], [vs], [c]), norm_sq=norm)
+        done.append((norm, ps, ms, vs, c))
+        for a, b in zip(done[0], done[-1]):
+            assert torch.equal(a, b), offs
+        done[1:] = []
