@@ -257,12 +257,12 @@ uint32_t q8_key(uint32_t seed, int64_t step) { return q8_mix(q8_mix(seed) + (uin
 // the entries of one tensor's pieces: `a` and `b` advance by their element
 // sizes, `copy` by 2 bytes
 template <typename Fill>
-int32_t add_q8(Q8Batch& batch, Fill& fill, int64_t tile, void* state, int64_t numel, int32_t index, const void* a, int64_t asz,
+int32_t add_q8(Q8Batch& batch, Fill& fill, void* state, int64_t numel, int32_t index, const void* a, int64_t asz,
                const void* b, int64_t bsz, const void* copy) {
     for (int64_t off = 0; off < numel; off += kLaunchElems) {
         const int64_t n = launch_piece(numel, off);
         int at = 0;
-        const int32_t rc = fill.add(ceil_div(n, tile), at);
+        const int32_t rc = fill.add(ceil_div(n, kQ8Pad), at);
         if (rc != ZS_OK) return rc;
         const void* const ptr[4] = {advance(a, off * asz), advance(b, off * bsz), state, advance(copy, off * 2)};
         Q8Entry& e = batch.e[at];
@@ -276,9 +276,8 @@ int32_t add_q8(Q8Batch& batch, Fill& fill, int64_t tile, void* state, int64_t nu
     return ZS_OK;
 }
 
-// Counts the elements whose streams start off a cache line: where they are most
-// of a list, tiles are taken in runs, and what is read of these streams is kept
-// for the neighbour that shares a line.
+// Counts the elements whose written streams start off a cache line: tiles are
+// taken in runs where they are most of a list.
 struct OffLine {
     int64_t elems = 0;
     void add(int64_t numel, const void* a, const void* b) {
@@ -336,7 +335,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
-        const int32_t rc = add_q8(b, fill, kQ8Pad, t.state_q8, t.numel, k, t.param, psz, t.grad, gsz, t.param_bf16);
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.param, psz, t.grad, gsz, t.param_bf16);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();
@@ -347,7 +346,7 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
                    void* hip_stream) {
     const int64_t total = list_total(list, count);
     if (total < 0 || !dtype_ok(dtype) || count > kQ8MaxCount) return ZS_EINVAL;
-    const int64_t sz = elem_size(dtype), tile = encode ? q8_encode_tile(total) : kQ8Pad;
+    const int64_t sz = elem_size(dtype);
     Ranges ranges;
     OffLine off_line;
     if (!ranges.reserve(count, 3)) return ZS_EINVAL;
@@ -365,17 +364,17 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
     if (ranges.clash()) return ZS_EOVERLAP;
     Q8Batch b;
     std::memset(&b, 0, sizeof(b));
-    b.runs = off_line.most_of(total);   // (of a storing one: whether it keeps what it reads)
+    b.runs = encode ? 0 : off_line.most_of(total);
     b.sc.key = q8_key(seed, 0);
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
-        return encode ? launch_q8_encode(x, dtype == ZS_BF16, x.runs != 0, tile, tiles, as_stream(hip_stream))
+        return encode ? launch_q8_encode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream))
                       : launch_q8_decode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream));
     };
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
         if (!encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr) continue;
-        const int32_t rc = add_q8(b, fill, tile, t.state_q8, t.numel, k, t.exp_avg, sz, t.exp_avg_sq, sz, nullptr);
+        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.exp_avg, sz, t.exp_avg_sq, sz, nullptr);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();

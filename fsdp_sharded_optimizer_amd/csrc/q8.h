@@ -24,10 +24,10 @@ __device__ __forceinline__ uint32_t q8_group(uint64_t group, uint32_t tensor_key
     return (uint32_t)group + (uint32_t)(group >> 32) * kGolden + tensor_key;
 }
 
-// The largest of the 64 lanes' values, for 4 or 8 values at once: x[k]'s result
-// ends in lane max_lane(k).  Each step halves the registers while it reduces:
-// after exchanging the halves (rows) of two registers, one maximum reduces both.
-// 10 or 22 operations in all, against 6 for each value by itself.
+// The largest of the 64 lanes' values, for 4 values at once: x[k]'s result ends
+// in lane max_lane(k).  Each step halves the registers while it reduces: after
+// exchanging the halves (rows) of two registers, one maximum reduces both.  10
+// operations in all, against 6 for each value by itself.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {   // lanes 0-31: a, 32-63: b
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -41,22 +41,13 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t x) {   // CTRL: a permutation of the lanes
     return max2(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ uint32_t max_row_halves(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    return dpp_max<0x128>(max_rows(max_halves(a, b), max_halves(c, d)));   // row_ror:8
-}
-template <int N>
-__device__ __forceinline__ uint32_t wave_max(const uint32_t (&x)[N]) {
-    static_assert(N == 4 || N == 8, "");
-    uint32_t y = max_row_halves(x[0], x[1], x[2], x[3]);
-    if constexpr (N == 8) {
-        const uint32_t hi = max_row_halves(x[4], x[5], x[6], x[7]);
-        y = (threadIdx.x & 8) ? hi : y;
-    }
+__device__ __forceinline__ uint32_t wave_max(const uint32_t (&x)[4]) {
+    uint32_t y = dpp_max<0x128>(max_rows(max_halves(x[0], x[1]), max_halves(x[2], x[3])));   // row_ror:8
     y = dpp_max<0xB1>(y);      // quad_perm 1,0,3,2
     y = dpp_max<0x4E>(y);      // quad_perm 2,3,0,1
     return dpp_max<0x141>(y);  // row_half_mirror
 }
-__device__ constexpr int max_lane(int k) { return (k & 1) * 32 + (k & 2) * 8 + (k & 4) * 2; }
+__device__ constexpr int max_lane(int k) { return (k & 1) * 32 + (k & 2) * 8; }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t max4(const float (&x)[4]) {

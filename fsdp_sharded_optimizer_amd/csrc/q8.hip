@@ -25,31 +25,31 @@ constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per chunk
 // CU, all it takes) / 6 / 7 / 8 / 9 / 11 / 12 KiB: the step on 809M fp32 parameters
 // (bf16 gradients, re-casts) 74.3 / 76.7 / 77.5 / 78.9 / 79.8 / 79.0 / 75.7; on 855M
 // bf16 parameters 79.7 / 80.7 / 81.4 / 79.5 / 77.4 / 73.3 / 67.1; reading 855M moments
-// out 80.2 / 80.9 / 78.1 / 74.2 / 69.1; storing 317M 69.3 at 0, 71.4 at 5, 61.4 at 6.
+// out 80.2 / 80.9 / 78.1 / 74.2 / 69.1; storing 406M bf16 moments 83 / 83 / 80 / 73 / 68,
+// fp32 ones 77 / 78 / 79 / 80 / 82 / 83 / 78.
 // (2 or 4 waves per workgroup: 0.5-4 points slower; plain instead of streaming
 // code accesses: the step 1 point slower.)  Launches of fewer than 2^25 elements
 // are not long enough for a cap to help.
 template <bool PBF16> constexpr unsigned kStepLds = PBF16 ? 7168 : 9216;
 constexpr unsigned kDecodeLds = 6144;
-constexpr unsigned kEncodeLds = 5120;
+constexpr unsigned kEncodeLds = 11264;   // of fp32 moments
 constexpr int64_t kCapElems = int64_t(1) << 25;
 unsigned cap(unsigned lds, int64_t elems) { return elems < kCapElems ? 0 : lds; }
 
-// Where a wave works: its tensor's entry and its CHUNKS chunks.
+// Where a wave works: its tensor's entry and its chunk.
 struct Chunk {
     Q8Entry e;
-    int64_t first;     // of the entry, of the wave's elements
+    int64_t first;     // of the entry, of the chunk's elements
     int64_t i;         // of the lane's elements in the first block
-    uint8_t* codes;    // the lane's exp_avg codes in the first chunk
-    uint8_t* scales;   // the first chunk's
+    uint8_t* codes;    // the lane's exp_avg codes
+    uint8_t* scales;   // the chunk's
 };
-template <int CHUNKS>
 __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b, bool runs) {
     const uint32_t w = runs ? tile_in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     uint32_t first_tile;
     const Q8Entry e = b.e[find_tensor(b.tab, w, first_tile)];
     const Q8At at = q8_at(e);
-    const int64_t first = (int64_t)(w - first_tile) * (CHUNKS * kQ8Pad);
+    const int64_t first = (int64_t)(w - first_tile) * kQ8Pad;
     return Chunk{e, first, first + threadIdx.x * 4, at.codes + 2 * first + threadIdx.x * (4 * kBlocks),
                  at.scales + first / (kQ8Block / 2)};
 }
@@ -105,38 +105,31 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__bui
 __device__ __forceinline__ uint32_t scale_m(uint32_t s, int b) { return (s >> (16 * b)) & 0xFFu; }
 __device__ __forceinline__ uint32_t scale_v(uint32_t s, int b) { return (s >> (16 * b + 8)) & 0xFFu; }
 
-// Stores the moments of a wave's chunks: the blocks' scales from their largest
+// Stores the moments of a wave's chunk: the blocks' scales from their largest
 // magnitudes, then the codes.
-template <int CHUNKS>
-__device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, const float (&m)[CHUNKS * kBlocks][4],
-                                              const float (&v)[CHUNKS * kBlocks][4]) {
-    constexpr int kAll = CHUNKS * kBlocks;
-    uint32_t most[2 * kAll];
+__device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, const float (&m)[kBlocks][4],
+                                              const float (&v)[kBlocks][4]) {
+    uint32_t most[2 * kBlocks];
 #pragma unroll
-    for (int b = 0; b < kAll; ++b) most[2 * b] = max4(m[b]), most[2 * b + 1] = max4(v[b]);
+    for (int b = 0; b < kBlocks; ++b) most[2 * b] = max4(m[b]), most[2 * b + 1] = max4(v[b]);
     const uint32_t e = q8_scale(wave_max(most));
     const uint32_t tensor_key = q8_mix(key + (c.e.index_off & 0xFFFFFFu) * kGolden);
     // the wave's first group; its groups share the upper 32 bits
     const uint32_t group =
         q8_group(((uint64_t)(c.e.index_off >> 24) * kLaunchElems + (uint64_t)c.first) / 4, tensor_key);
+    uint32_t mc[kBlocks], vc[kBlocks], scales = 0;
 #pragma unroll
-    for (int h = 0; h < CHUNKS; ++h) {
-        if (h > 0 && c.first + h * kQ8Pad >= (int64_t)c.e.numel) return;   // past the padded state
-        uint32_t mc[kBlocks], vc[kBlocks], scales = 0;
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-            const int b = h * kBlocks + k;
-            const uint32_t em = (uint32_t)__builtin_amdgcn_readlane((int)e, max_lane(2 * b));
-            const uint32_t ev = (uint32_t)__builtin_amdgcn_readlane((int)e, max_lane(2 * b + 1));
-            const uint32_t word = q8_mix(group + b * (uint32_t)(kQ8Block / 4) + threadIdx.x);
-            mc[k] = q8_encode4<kTopM>(m[b], em, word);
-            vc[k] = q8_encode4<kTopV>(v[b], ev, word);
-            scales |= (em | ev << 8) << (16 * k);
-        }
-        store_codes(c.codes + h * 2 * kQ8Pad, mc);
-        store_codes(c.codes + h * 2 * kQ8Pad + kQ8Pad, vc);
-        if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(c.scales)[h] = scales;
+    for (int b = 0; b < kBlocks; ++b) {
+        const uint32_t em = (uint32_t)__builtin_amdgcn_readlane((int)e, max_lane(2 * b));
+        const uint32_t ev = (uint32_t)__builtin_amdgcn_readlane((int)e, max_lane(2 * b + 1));
+        const uint32_t word = q8_mix(group + b * (uint32_t)(kQ8Block / 4) + threadIdx.x);
+        mc[b] = q8_encode4<kTopM>(m[b], em, word);
+        vc[b] = q8_encode4<kTopV>(v[b], ev, word);
+        scales |= (em | ev << 8) << (16 * b);
     }
+    store_codes(c.codes, mc);
+    store_codes(c.codes + kQ8Pad, vc);
+    if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(c.scales) = scales;
 }
 
 // u / step_size of one element from its new moments
@@ -218,12 +211,12 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
         store4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
         if (!PBF16 && copy != nullptr) store4(copy, c.i + k * kQ8Block, n, WHOLE, p[k]);
     }
-    store_moments<1>(c, sc.key, m, v);
+    store_moments(c, sc.key, m, v);
 }
 
 template <bool PBF16, bool GBF16, bool DEV, bool KEEP, bool RUNS>
 __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
-    const Chunk c = chunk_of<1>(b, RUNS);
+    const Chunk c = chunk_of(b, RUNS);
     const Q8Scalars sc = DEV ? *b.sc_dev : b.sc;
     if (c.first + kQ8Pad <= (int64_t)c.e.numel && sc.adamw.eps >= kFastEps)
         step_chunk<PBF16, GBF16, true, true, KEEP, RUNS>(b, sc, c);
@@ -231,33 +224,40 @@ __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
         step_chunk<PBF16, GBF16, false, false, KEEP, RUNS>(b, sc, c);
 }
 
-template <bool BF16, int CHUNKS, bool KEEP>
+template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
-    constexpr int kAll = CHUNKS * kBlocks;
-    const Chunk c = chunk_of<CHUNKS>(b, false);
+    const Chunk c = chunk_of(b, false);
     const int64_t n = c.e.numel;
-    const bool whole = c.first + CHUNKS * kQ8Pad <= n;
+    const bool whole = c.first + kQ8Pad <= n;
     const T* const from_m = unpack_ptr<const T>(c.e.lo[0], c.e.hi[0]);
     const T* const from_v = unpack_ptr<const T>(c.e.lo[1], c.e.hi[0] >> 16);
-    float m[kAll][4] = {}, v[kAll][4] = {};
+    float m[kBlocks][4] = {}, v[kBlocks][4] = {};
+    if (whole && from_m != nullptr && from_v != nullptr) {   // no branch between the loads
 #pragma unroll
-    for (int k = 0; k < kAll; ++k) {
-        const int64_t i = c.i + k * kQ8Block;
-        if (from_m != nullptr) load4<KEEP>(from_m, i, n, whole, m[k]);
-        if (from_v != nullptr) load4<KEEP>(from_v, i, n, whole, v[k]);
+        for (int k = 0; k < kBlocks; ++k) {
+            load4<false>(from_m, c.i + k * kQ8Block, n, true, m[k]);
+            load4<false>(from_v, c.i + k * kQ8Block, n, true, v[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            const int64_t i = c.i + k * kQ8Block;
+            if (from_m != nullptr) load4<false>(from_m, i, n, false, m[k]);
+            if (from_v != nullptr) load4<false>(from_v, i, n, false, v[k]);
+        }
     }
 #pragma unroll
-    for (int k = 0; k < kAll; ++k)
+    for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[k][j] = __uint_as_float(magnitude(v[k][j]));
-    store_moments<CHUNKS>(c, b.sc.key, m, v);
+    store_moments(c, b.sc.key, m, v);
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
-    const Chunk c = chunk_of<1>(b, b.runs != 0);
+    const Chunk c = chunk_of(b, b.runs != 0);
     const int64_t n = c.e.numel;
     const bool whole = c.first + kQ8Pad <= n;
     uint32_t mc[kBlocks], vc[kBlocks];
@@ -312,22 +312,12 @@ hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, bool
                      : launch_step<false, false>(b, keep, tiles, stream);
 }
 
-template <bool BF16, bool KEEP>
-static hipError_t encode(const Q8Batch& b, int64_t tile, int64_t tiles, hipStream_t stream) {
+hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    if (tile == kQ8Pad) hipLaunchKernelGGL((q8_encode_kernel<BF16, 1, KEEP>), grid, block, 0, stream, b);
-    else hipLaunchKernelGGL((q8_encode_kernel<BF16, 2, KEEP>), grid, block, kEncodeLds, stream, b);
+    const unsigned lds = cap(bf16 ? 0 : kEncodeLds, tiles * kQ8Pad);
+    if (bf16) hipLaunchKernelGGL(q8_encode_kernel<true>, grid, block, lds, stream, b);
+    else hipLaunchKernelGGL(q8_encode_kernel<false>, grid, block, lds, stream, b);
     return hipGetLastError();
-}
-
-// Two chunks per wave for long lists: 317M moments stored in 333 us, 352 with one
-// (one is as fast up to 34M elements, and faster below 4M).
-int64_t q8_encode_tile(int64_t total) { return total < kCapElems ? kQ8Pad : 2 * kQ8Pad; }
-
-// keep: 405M moments at odd offsets 714 -> 691 us (bf16 731 -> 703); aligned 648 -> 686
-hipError_t launch_q8_encode(const Q8Batch& b, int bf16, bool keep, int64_t tile, int64_t tiles, hipStream_t stream) {
-    if (bf16) return keep ? encode<true, true>(b, tile, tiles, stream) : encode<true, false>(b, tile, tiles, stream);
-    return keep ? encode<false, true>(b, tile, tiles, stream) : encode<false, false>(b, tile, tiles, stream);
 }
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {

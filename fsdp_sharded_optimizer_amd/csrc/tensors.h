@@ -209,13 +209,9 @@ struct Q8Batch {
     Q8Scalars sc;                // the conversions use the key alone
 };
 static_assert(sizeof(Q8Batch) <= 4096, "kernel arguments");
-// elements per workgroup of the storing conversion, for a list of that many in
-// all (the step and the reading one: kQ8Pad)
-int64_t q8_encode_tile(int64_t total);
 hipError_t launch_adamw_q8(const Q8Batch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
                            hipStream_t stream);
-// keep: the moments lie off cache lines
-hipError_t launch_q8_encode(const Q8Batch& b, int bf16, bool keep, int64_t tile, int64_t tiles, hipStream_t stream);
+hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream);
 
 }  // namespace zs
