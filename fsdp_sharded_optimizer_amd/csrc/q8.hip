@@ -26,12 +26,14 @@ constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per chunk
 // (bf16 gradients, re-casts) 74.3 / 76.7 / 77.5 / 78.9 / 79.8 / 79.0 / 75.7; on 855M
 // bf16 parameters 79.7 / 80.7 / 81.4 / 79.5 / 77.4 / 73.3 / 67.1; reading 855M moments
 // out 80.2 / 80.9 / 78.1 / 74.2 / 69.1; storing 406M bf16 moments 83 / 83 / 80 / 73 / 68,
-// fp32 ones 77 / 78 / 79 / 80 / 82 / 83 / 78.
+// fp32 ones 77 / 78 / 79 / 80 / 82 / 83 / 78.  Tiles in runs, on 405M at odd offsets:
+// fp32 parameters 66 / 68 / 68 / 67 / 68 / 71 / 72 and 69 at 14, bf16 ones 74 / 76 / 75 / 71 /
+// 71 / 68 / 63, reading out 63 / 67 / 71 / 67 / 64 / 58 / 53.
 // (2 or 4 waves per workgroup: 0.5-4 points slower; plain instead of streaming
 // code accesses: the step 1 point slower.)  Launches of fewer than 2^25 elements
 // are not long enough for a cap to help.
-template <bool PBF16> constexpr unsigned kStepLds = PBF16 ? 7168 : 9216;
-constexpr unsigned kDecodeLds = 6144;
+template <bool PBF16, bool RUNS> constexpr unsigned kStepLds = PBF16 ? (RUNS ? 6144 : 7168) : (RUNS ? 12288 : 9216);
+constexpr unsigned kDecodeLds = 6144, kDecodeRunsLds = 7168;
 constexpr unsigned kEncodeLds = 11264;   // of fp32 moments
 constexpr int64_t kCapElems = int64_t(1) << 25;
 unsigned cap(unsigned lds, int64_t elems) { return elems < kCapElems ? 0 : lds; }
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
 template <bool PBF16, bool GBF16, bool KEEP, bool RUNS>
 hipError_t launch_step(const Q8Batch& b, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    const unsigned lds = cap(kStepLds<PBF16>, tiles * kQ8Pad);
+    const unsigned lds = cap(kStepLds<PBF16, RUNS>, tiles * kQ8Pad);
     if (b.sc_dev != nullptr)
         hipLaunchKernelGGL((adamw_q8_kernel<PBF16, GBF16, true, KEEP, RUNS>), grid, block, lds, stream, b);
     else
@@ -322,7 +324,7 @@ hipError_t launch_q8_encode(const Q8Batch& b, int bf16, int64_t tiles, hipStream
 
 hipError_t launch_q8_decode(const Q8Batch& b, int bf16, int64_t tiles, hipStream_t stream) {
     const dim3 grid((unsigned)tiles), block(kWave);
-    const unsigned lds = cap(kDecodeLds, tiles * kQ8Pad);
+    const unsigned lds = cap(b.runs ? kDecodeRunsLds : kDecodeLds, tiles * kQ8Pad);
     if (bf16) hipLaunchKernelGGL(q8_decode_kernel<true>, grid, block, lds, stream, b);
     else hipLaunchKernelGGL(q8_decode_kernel<false>, grid, block, lds, stream, b);
     return hipGetLastError();

@@ -51,9 +51,10 @@ __device__ __forceinline__ uint32_t find_tensor(const ListTable<N>& tab, uint32_
 // The tile of workgroup w of n when an XCD takes runs of 4 consecutive tiles
 // (gfx950 deals workgroups to its 8 XCDs in turn).  Where written streams do not
 // start on cache lines, neighbouring tiles write parts of one line, which is
-// then put together in one XCD's L2 instead of in memory: 405M parameters at odd
-// offsets, 8-bit step 1233 -> 1199 us (bf16 708 -> 689), read-out 494 -> 444.
-// On aligned tensors it costs 2-7 %.
+// then put together in one XCD's L2 instead of in memory: 405M moments read out
+// to odd offsets 507 -> 433 us, the 8-bit step 80 -> 76 at 25M fp32 parameters
+// (the same at 405M, whose parameters' lines are kept as well).  On aligned
+// tensors it costs 2-7 %.
 __device__ __forceinline__ uint32_t tile_in_runs(uint32_t w, uint32_t n) {
     constexpr uint32_t kRun = 4, kAll = 8 * kRun;
     const uint32_t base = w / kAll * kAll, i = w % kAll;
