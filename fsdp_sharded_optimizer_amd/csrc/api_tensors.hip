@@ -161,18 +161,28 @@ T* advance(T* p, int64_t bytes) {
     return p == nullptr ? nullptr : reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
 }
 
-// Elements to start before a tensor's first one so that, after them, every
-// stream that is read and written is on a cache line (offsets in elements from
-// a line agree across the streams); 0 where they do already or do not agree.
-// A read-modify-write stream whose waves share lines runs a quarter slower.
+// Elements that tile 0 starts before a tensor's first one, so that the moments'
+// tiles (most of the bytes) start on whole tiles, 1 KiB, and with them every
+// stream at the same offset in elements (views of flat buffers).  405M fp32
+// parameters with re-casts, 32 / 33 / 128 elements off: 1687 / 1707 / 1685 us, with
+// cache lines alone 1764 / 1843 / 1800 (aligned 1692).  Moments that do not share
+// their offset from a cache line: the parameter's.
 constexpr int64_t kLine = 128;
-int64_t line_shift(const zs_adamw_tensor& t, int64_t psz) {
-    const int64_t per = kLine / psz;   // elements of param in a line (64 bf16 or 32 fp32)
-    const int64_t off = (int64_t)(addr(t.param) % kLine) / psz;
-    for (const float* s : {t.exp_avg, t.exp_avg_sq})
-        if ((int64_t)(addr(s) % kLine) / 4 != off % 32) return 0;
-    return off == 0 ? 0 : kListTile - (per - off);
+int64_t tile_shift(const zs_adamw_tensor& t, int64_t psz) {
+    const uintptr_t m = addr(t.exp_avg) / 4, v = addr(t.exp_avg_sq) / 4;
+    return (int64_t)(m % 32 == v % 32 ? m : addr(t.param) / (uintptr_t)psz) % kListTile;
 }
+
+// Counts the elements whose tiles start off a cache line in some stream: lists
+// of which they are the most run differently (tile_in_runs, residency, caching).
+struct OffLine {
+    int64_t elems = 0;
+    // the addresses of the tiles' start, as bits of them all
+    void add(int64_t numel, uintptr_t a) {
+        if (a % kLine != 0) elems += numel;
+    }
+    bool most_of(int64_t total) const { return elems > total / 2; }
+};
 
 // Whether b's elements come right after a's first n in every stream: the update
 // knows no tensors, so the two are one entry then (views of flat buffers: 25M
@@ -194,6 +204,7 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
     }
     const int64_t psz = elem_size(param_dtype), gsz = elem_size(grad_dtype);
     Ranges ranges;
+    OffLine off_line;
     if (!ranges.reserve(count, 5)) return ZS_EINVAL;
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_tensor& t = list[k];
@@ -211,6 +222,10 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
         ranges.add(2, t.exp_avg, t.numel * 4, true);
         ranges.add(3, t.exp_avg_sq, t.numel * 4, true);
         ranges.add(4, t.param_bf16, t.numel * 2, true);
+        const uintptr_t shift = (uintptr_t)tile_shift(t, psz);
+        off_line.add(t.numel, (addr(t.param) - shift * (uintptr_t)psz) | (addr(t.grad) - shift * (uintptr_t)gsz) |
+                                  (addr(t.exp_avg) - shift * 4) | (addr(t.exp_avg_sq) - shift * 4) |
+                                  (t.param_bf16 == nullptr ? 0 : addr(t.param_bf16) - shift * 2));
     }
     ranges.add_read(norm_sq_dev, 8);
     ranges.add_read(sc_dev, (int64_t)sizeof(zs_adamw_scalars));
@@ -219,11 +234,11 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
     AdamwBatch b;
     std::memset(&b, 0, sizeof(b));
     if (sc_dev == nullptr) b.sc = make_scalars(hp);
-    const bool keep = keep_grads(total * gsz);
+    const bool off = off_line.most_of(total), keep = off || keep_grads(total * gsz);
     b.sc_dev = reinterpret_cast<const AdamwScalars*>(sc_dev);
     b.norm_sq = norm_sq_dev;
     auto launch = [&](const AdamwBatch& x, int64_t tiles) {
-        return launch_adamw_tensors(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, keep, tiles,
+        return launch_adamw_tensors(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, keep, off, tiles,
                                     as_stream(hip_stream));
     };
     Filler<AdamwBatch, decltype(launch)> fill(b, launch);
@@ -233,7 +248,7 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
         if (numel == 0) continue;
         while (k + 1 < count && (list[k + 1].numel == 0 || follows(t, numel, list[k + 1], psz, gsz)))
             numel += list[++k].numel;
-        const int64_t shift = line_shift(t, psz);
+        const int64_t shift = tile_shift(t, psz);
         for (int64_t off = 0; off < numel; off += kLaunchElems) {
             const int64_t n = launch_piece(numel, off);
             int at = 0;
@@ -276,16 +291,6 @@ int32_t add_q8(Q8Batch& batch, Fill& fill, void* state, int64_t numel, int32_t i
     return ZS_OK;
 }
 
-// Counts the elements whose written streams start off a cache line: tiles are
-// taken in runs where they are most of a list.
-struct OffLine {
-    int64_t elems = 0;
-    void add(int64_t numel, const void* a, const void* b) {
-        if (!aligned(a, kLine) || !aligned(b, kLine)) elems += numel;
-    }
-    uint32_t most_of(int64_t total) const { return elems > total / 2 ? 1 : 0; }
-};
-
 int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_scalars* sc_dev,
                         const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                         const double* norm_sq_dev, void* hip_stream) {
@@ -313,7 +318,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         ranges.add(1, t.grad, t.numel * gsz, false);
         ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), true);
         ranges.add(3, t.param_bf16, t.numel * 2, true);
-        off_line.add(t.numel, t.param, t.param_bf16);
+        off_line.add(t.numel, addr(t.param) | addr(t.param_bf16));
     }
     ranges.add_read(norm_sq_dev, 8);
     ranges.add_read(sc_dev, (int64_t)sizeof(zs_adamw_q8_scalars));
@@ -359,12 +364,12 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
         ranges.add(0, t.exp_avg, t.numel * sz, !encode);
         ranges.add(1, t.exp_avg_sq, t.numel * sz, !encode);
         ranges.add(2, t.state_q8, moments_q8_bytes(t.numel), encode);
-        off_line.add(t.numel, t.exp_avg, t.exp_avg_sq);
+        off_line.add(t.numel, addr(t.exp_avg) | addr(t.exp_avg_sq));
     }
     if (ranges.clash()) return ZS_EOVERLAP;
     Q8Batch b;
     std::memset(&b, 0, sizeof(b));
-    b.runs = encode ? 0 : off_line.most_of(total);
+    b.runs = !encode && off_line.most_of(total);
     b.sc.key = q8_key(seed, 0);
     auto launch = [&](const Q8Batch& x, int64_t tiles) {
         return encode ? launch_q8_encode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream))

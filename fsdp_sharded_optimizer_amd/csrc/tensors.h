@@ -154,9 +154,8 @@ hipError_t launch_norm_tensors(const NormBatch& b, int grad_bf16, bool keep, int
                                double* partials, hipStream_t stream);
 
 // --- AdamW, fp32 moments --------------------------------------------------
-// Tile 0 of a tensor starts `shift` elements before its first one, so that the
-// other tiles start on cache lines of every stream that is read and written
-// (0 where the tensor's streams do, or cannot all).
+// Tile 0 of a tensor starts `shift` elements before its first one, for the
+// alignment of the tiles (less than one tile).
 struct AdamwEntry {
     uint32_t lo[5];   // param, grad, exp_avg, exp_avg_sq, bf16 re-cast (0: none)
     uint32_t hi[3];   // param | grad << 16, exp_avg | exp_avg_sq << 16, re-cast | shift << 16
@@ -171,8 +170,9 @@ struct AdamwBatch {
 };
 constexpr int64_t kListTile = 256;
 static_assert(sizeof(AdamwBatch) <= 4096, "kernel arguments");
-hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, bool keep, int64_t tiles,
-                                hipStream_t stream);
+// keep: of the gradients; off_line: most tiles start off a cache line in some stream
+hipError_t launch_adamw_tensors(const AdamwBatch& b, int param_bf16, int grad_bf16, bool keep, bool off_line,
+                                int64_t tiles, hipStream_t stream);
 
 // --- 8-bit moments --------------------------------------------------------
 // Layout of one tensor's buffer of n elements, P = n rounded up to kQ8Pad:

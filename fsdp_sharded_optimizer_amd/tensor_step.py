@@ -28,23 +28,30 @@ from . import tensors as zt
 
 def _moments_like(params: Sequence[torch.Tensor]) -> list:
     """fp32 zeros for each tensor, views of one buffer.  Each starts at its
-    parameter's element offset from a 128-byte boundary, so that the step can
-    put every stream it reads and writes on whole cache lines; those of
-    parameters that follow one another do so too."""
-    spots, at = [], 0
+    parameter's element offset from a boundary of 256 elements, so that the step
+    can put every stream it reads and writes on whole tiles; those of parameters
+    that follow one another do so too."""
+    buffer = torch.zeros(sum(p.numel() + 256 for p in params) + 256, dtype=torch.float32, device=params[0].device)
+    first, views = buffer.data_ptr() // 4, []
+    at = 0
     for p in params:
-        at += (p.data_ptr() % 128 // p.element_size() - at) % 32
-        spots.append(at)
+        at += (p.data_ptr() // p.element_size() - first - at) % 256
+        views.append(buffer[at:at + p.numel()])
         at += p.numel()
-    buffer = torch.zeros(max(at, 1), dtype=torch.float32, device=params[0].device)
-    return [buffer[a:a + p.numel()] for a, p in zip(spots, params)]
+    return views
 
 
 def _states_for(params: Sequence[torch.Tensor]) -> list:
-    """Zeroed 8-bit moments for each tensor, views of one buffer on 128-byte boundaries."""
+    """Zeroed 8-bit moments for each tensor, views of one buffer, each on a
+    boundary of 1 KiB (what a wave reads of them at once)."""
     sizes = [zt.moments_q8_bytes(p.numel()) for p in params]
-    buffer = torch.zeros(max(sum(sizes), 1), dtype=torch.uint8, device=params[0].device)
-    return list(buffer[:sum(sizes)].split(sizes))
+    room = [-(-n // 1024) * 1024 for n in sizes]
+    buffer = torch.zeros(sum(room) + 1024, dtype=torch.uint8, device=params[0].device)
+    at, views = -buffer.data_ptr() % 1024, []
+    for n, r in zip(sizes, room):
+        views.append(buffer[at:at + n])
+        at += r
+    return views
 
 
 def _written(params: Sequence[torch.Tensor], copies) -> tuple:

@@ -15,8 +15,8 @@
  * numel >= 0, the sum at most 2^39; a tensor with numel 0 is skipped (its
  * pointers are not looked at).  Every tensor is contiguous, fp32 pointers are
  * 4-byte and bf16 pointers 2-byte aligned; views at any element offset are
- * fine (full speed: what is read and written at one common offset from a
- * 128-byte boundary, any offset for the rest).  A buffer that is written must
+ * fine (full speed: every stream at one common offset, in elements, from a
+ * boundary of 256).  A buffer that is written must
  * not overlap any other buffer of the list (ZS_EOVERLAP); buffers that are
  * only read may overlap one another (two tensors may share one gradient).
  */
@@ -113,7 +113,7 @@ ZS_API int32_t adamw_step_tensors_dev(const zs_adamw_scalars* scalars_dev, const
  * (i % 4) * 0x9E3779B9;  r = h >> 12 for exp_avg, h & 0xFFFFF for exp_avg_sq.
  * The order of codes and scales in the buffer is the library's own.  A buffer
  * of zero bytes holds zero moments.  Buffers are 16-byte aligned (full speed:
- * 128) and hold moments_q8_bytes(numel) bytes.
+ * 1 KiB) and hold moments_q8_bytes(numel) bytes.
  */
 #define ZS_Q8_BLOCK 256
 
@@ -167,7 +167,7 @@ typedef struct {
  * 32 bits of hp->step: the same call on the same data gives the same bits.
  * A non-finite norm leaves every tensor and its moments unchanged; without a
  * norm a gradient that is not finite makes its whole block's moments NaN.
- * Full speed: param, and param_bf16, on a 128-byte boundary.
+ * Full speed: param, grad and param_bf16 on boundaries of 256 elements.
  */
 ZS_API int32_t adamw_step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_tensor* tensors,
                                      int32_t count, int32_t param_dtype, int32_t grad_dtype,

@@ -305,3 +305,28 @@ def test_a_captured_step_follows_the_optimizer_or_refuses(bits):
     plain.max_norm = 1.0
     with pytest.raises(ValueError):
         graph.replay()
+
+
+def test_the_state_s_layout():
+    """Moments at their parameters' offsets from a boundary of 256 elements,
+    neighbours kept next to one another; 8-bit moments on boundaries of 1 KiB;
+    nothing overlaps."""
+    flat = torch.zeros(9000, device="cuda")
+    params = [flat[3:1000], flat[1000:1001], flat[1001:5000], flat[6000:6300].clone(), torch.zeros(0, device="cuda"),
+              flat[7001:8999]]
+    opt = zs.TensorOptimizer(params, lr=1e-3)
+    for ts in opt.moments():
+        ends = 0
+        for p, t in zip(params, ts):
+            if t.numel():
+                assert t.data_ptr() // 4 % 256 == p.data_ptr() // 4 % 256 and t.data_ptr() >= ends
+                ends = t.data_ptr() + 4 * t.numel()
+        assert ts[1].data_ptr() == ts[0].data_ptr() + 4 * 997 and ts[2].data_ptr() == ts[1].data_ptr() + 4
+        assert all(not t.any() for t in ts)
+    opt = zs.TensorOptimizer(params, lr=1e-3, state_bits=8)
+    ends = 0
+    for p, s in zip(params, opt._states):
+        assert s.numel() == zs.moments_q8_bytes(p.numel())
+        if s.numel():
+            assert s.data_ptr() % 1024 == 0 and s.data_ptr() >= ends
+            ends = s.data_ptr() + s.numel()

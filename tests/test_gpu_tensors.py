@@ -445,3 +445,31 @@ def test_long_gradients_at_any_offset(gdtype, n):
         for a, b in zip(done[0], done[-1]):
             assert torch.equal(a, b), offs
         done[1:] = []
+
+
+@pytest.mark.parametrize("gdtype,pdtype,copy", [(torch.float32, torch.float32, False), (torch.bfloat16, torch.float32, True),
+                                                (torch.bfloat16, torch.bfloat16, False)])
+def test_step_at_every_kind_of_offset(gdtype, pdtype, copy):
+    """Streams at one offset from a tile, at two, and at offsets of their own;
+    lengths around a tile."""
+    for n in (1, 255, 256, 257, 600):
+        pools, *_ = a_list([n], pdtype, gdtype, copy, None, seed=n)
+        hp = zs.AdamWConfig(**HP, step=2)
+        want = one_by_one(pools, hp, None)[0]
+        for offs in ((0,) * 5, (1,) * 5, (31,) * 5, (128,) * 5, (255,) * 5, (0, 0, 255, 255, 0), (7, 0, 32, 64, 1),
+                     (64, 3, 31, 32, 5)):
+            names = "pgmvc" if copy else "pgmv"
+            guarded = {}
+            for name, off in zip(names, offs):
+                x = pools[name].views[0]
+                buffer = torch.full((n + 600,), 7.75, dtype=x.dtype, device="cuda")
+                buffer[256 + off:256 + off + n] = x
+                guarded[name] = buffer
+            at = {name: b[256 + off:256 + off + n] for (name, b), off in zip(guarded.items(), offs)}
+            zs.adamw_step_tensors(hp, zs.AdamWTensors([at["p"]], [at["g"]], [at["m"]], [at["v"]],
+                                                      [at["c"]] if copy else None))
+            for name, off in zip(names, offs):
+                if name != "g":
+                    assert same_bits(at[name], want[name]), (n, offs, name)
+                b = guarded[name]
+                assert bool((b[:256 + off] == 7.75).all()) and bool((b[256 + off + n:] == 7.75).all()), (n, offs, name)
