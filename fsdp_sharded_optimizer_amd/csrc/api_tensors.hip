@@ -116,7 +116,7 @@ public:
     Filler(Batch& b, Launch launch) : b_(b), launch_(launch) { clear(); }
     // room for an entry of `tiles` workgroups; the entry's place in out
     int32_t add(int64_t tiles, int& out) {
-        if (count_ == decltype(b_.tab)::kMax || tiles_ + tiles > kListMaxTiles) {
+        if (count_ == Table::kMax || tiles_ + tiles > kListMaxTiles) {
             const int32_t rc = flush();
             if (rc != ZS_OK) return rc;
         }
@@ -130,11 +130,12 @@ public:
         auto& tab = b_.tab;
         tab.shift = 0;
         while (((tiles_ - 1) >> tab.shift) >= kListBuckets) ++tab.shift;
+        constexpr int kPer = Table::kPerWord;
         std::memset(tab.bucket, 0, sizeof(tab.bucket));
         int t = 0;
         for (int part = 0; part < kListBuckets && ((int64_t)part << tab.shift) < tiles_; ++part) {
             while ((int64_t)tab.start[t + 1] <= ((int64_t)part << tab.shift)) ++t;
-            tab.bucket[part / 4] |= (uint32_t)t << (8 * (part % 4));
+            tab.bucket[part / kPer] |= (uint32_t)t << (Table::kBits * (part % kPer));
         }
         const int32_t rc = hip_status(launch_(b_, tiles_));
         clear();
@@ -142,8 +143,8 @@ public:
     }
 
 private:
+    using Table = decltype(Batch::tab);
     void clear() {
-        static_assert(decltype(b_.tab)::kMax <= 255, "a bucket names a tensor in a byte");
         for (uint32_t& s : b_.tab.start) s = kNoTile;
         count_ = 0;
         tiles_ = 0;
@@ -401,7 +402,7 @@ extern "C" {
 int64_t grad_norm_sq_tensors_workspace_bytes(const zs_tensor* grads, int32_t count, int32_t grad_dtype) {
     const int64_t parts = norm_partials_of(grads, count, grad_dtype);
     if (parts < 0) return -1;
-    return (parts <= kSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
+    return (parts <= kListSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
 }
 
 int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad_dtype, double grad_scale,
@@ -445,11 +446,11 @@ int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad
             const int32_t rc = fill.add(ceil_div(n, tile), at);
             if (rc != ZS_OK) return rc;
             const void* const p = advance(grads[k].ptr, off * gsz);
-            b.e[at] = NormEntry{ptr_lo(p), ptr_hi(p), (uint32_t)n};
+            b.e[at] = NormEntry{ptr_lo(p), ptr_hi(p) | (uint32_t)((n - 1) % tile) << 16};
         }
     const int32_t rc = fill.flush();
     if (rc != ZS_OK || parts == 1) return rc;
-    return hip_status(launch_sum_partials(partials, parts, partials + parts, out_sq_dev, as_stream(hip_stream)));
+    return hip_status(launch_list_sum(partials, parts, partials + parts, out_sq_dev, as_stream(hip_stream)));
 }
 
 int32_t adamw_step_tensors(const zs_adamw* hp, const zs_adamw_tensor* tensors, int32_t count, int32_t param_dtype,

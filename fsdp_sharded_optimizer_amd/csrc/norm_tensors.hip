@@ -25,7 +25,7 @@ template <bool BF16> constexpr int64_t kTile = (int64_t)kBlock * kVec<BF16> * kQ
 
 // the elements from `at` of n that a 128-bit load would bring, zeros past the end
 template <bool BF16>
-__device__ __forceinline__ u32x4 last_words(const typename GradType<BF16>::T* grad, int64_t at, int64_t n) {
+__device__ __forceinline__ u32x4 last_words(const typename GradType<BF16>::T* grad, int at, int n) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -44,13 +44,15 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     constexpr int VE = kVec<BF16>;
     using T = typename GradType<BF16>::T;
     uint32_t first;
-    const NormEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
-    const T* const grad = unpack_ptr<const T>(e.lo, e.hi);
-    const int64_t n = e.numel;
-    const int64_t tile = (int64_t)(blockIdx.x - first) * kTile<BF16>;
-    const int64_t lane0 = tile + threadIdx.x * VE;
+    const uint32_t t = find_tensor(b.tab, blockIdx.x, first);
+    const NormEntry e = b.e[t];
+    const uint32_t next = min(b.tab.start[t + 1], gridDim.x);
+    const T* const grad = unpack_ptr<const T>(e.lo, e.hi_tail) + (int64_t)(blockIdx.x - first) * kTile<BF16>;
+    const bool last = blockIdx.x + 1 == next;
+    const int n = last ? (int)(e.hi_tail >> 16) + 1 : (int)kTile<BF16>;   // the tile's elements
+    const int lane0 = threadIdx.x * VE;
     u32x4 v[kQ];
-    if (BF16 && (e.lo & 2) && tile + kTile<BF16> < n) {
+    if (BF16 && (e.lo & 2) && !last) {
         // bf16 at an odd offset: a lane's 16 bytes would span 5 words.  The words
         // from its second element on instead; its first element is in the last
         // word of the lane before (of a wave's first lane: loaded by itself).
@@ -68,13 +70,13 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
             v[q] = u32x4{__builtin_amdgcn_alignbit(w.x, before, 16), __builtin_amdgcn_alignbit(w.y, w.x, 16),
                          __builtin_amdgcn_alignbit(w.z, w.y, 16), __builtin_amdgcn_alignbit(w.w, w.z, 16)};
         }
-    } else if (tile + kTile<BF16> <= n) {
+    } else if (n == (int)kTile<BF16>) {
 #pragma unroll
         for (int q = 0; q < kQ; ++q) v[q] = ld_u32x4_any<KEEP>(grad + lane0 + q * kBlock * VE);
     } else {   // a tensor's ragged last tile: elements past the end add +0
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
-            const int64_t at = lane0 + q * kBlock * VE;
+            const int at = lane0 + q * kBlock * VE;
             if (at + VE <= n) v[q] = ld_u32x4_any<KEEP>(grad + at);
             else v[q] = last_words<BF16>(grad, at, n);
         }
@@ -99,7 +101,40 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     if (threadIdx.x == 0) partials[xcd_slot(blockIdx.x, gridDim.x)] = total;
 }
 
+// Up to kListSumOneGroup partials in one workgroup, in a fixed order: thread i adds
+// the partials i, i + 1024, ..., then the butterfly of its wave, then the waves.
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void list_sum_kernel(const double* __restrict__ partials, int count,
+                                                               double* __restrict__ out) {
+    __shared__ double part[kSumThreads / 64];
+    constexpr int kMost = (int)(kListSumOneGroup / kSumThreads);
+    double x[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+        const int i = threadIdx.x + k * kSumThreads;
+        x[k] = i < count ? partials[i] : 0.0;
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) s += x[k];
+    s = wave_sum(s);
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+#pragma unroll
+        for (int w = 0; w < kSumThreads / 64; ++w) s += part[w];
+        *out = s;
+    }
+}
+
 }  // namespace
+
+hipError_t launch_list_sum(const double* partials, int64_t count, double* stage, double* out, hipStream_t stream) {
+    if (count <= kSumOneGroup || count > kListSumOneGroup) return launch_sum_partials(partials, count, stage, out, stream);
+    hipLaunchKernelGGL(list_sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, partials, (int)count, out);
+    return hipGetLastError();
+}
 
 int64_t norm_tile_elems(int grad_bf16) { return grad_bf16 ? kTile<true> : kTile<false>; }
 

@@ -7,7 +7,7 @@
  * norm over the list, the AdamW update of every tensor with its moments in
  * fp32 or in 8 bits, and the conversions of 8-bit moments.  The list is read
  * during the call only: tables of it travel in the kernel arguments (98
- * tensors to a launch, 240 for the norm), so nothing is allocated on the
+ * tensors to a launch, 328 for the norm), so nothing is allocated on the
  * device, copied to it or kept, and a call can be captured into a HIP graph as
  * is.
  *

@@ -473,3 +473,40 @@ def test_step_at_every_kind_of_offset(gdtype, pdtype, copy):
                     assert same_bits(at[name], want[name]), (n, offs, name)
                 b = guarded[name]
                 assert bool((b[:256 + off] == 7.75).all()) and bool((b[256 + off + n:] == 7.75).all()), (n, offs, name)
+
+
+@pytest.mark.parametrize("count", [255, 256, 257, 327, 328, 329, 656, 1000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_of_many_tensors(dtype, count):
+    """Lists around what one table holds: empty tensors, one element, whole tiles
+    and ragged ones among them."""
+    tile = 8192 if dtype == torch.bfloat16 else 4096
+    kinds = [1, 0, 17, tile, tile + 1, 300, 2 * tile - 1, 8]
+    numels = [kinds[(k * k + k // 7) % 8] for k in range(count)]
+    gs = draws(numels, count, 0.1, dtype == torch.bfloat16)
+    want = math.fsum(math.fsum((x * np.float32(0.3)).astype(np.float64) ** 2) for x in gs)
+    got = set()
+    for packed in (None, 1):
+        out = torch.zeros(1, dtype=torch.float64, device="cuda")
+        zs.grad_norm_sq_tensors(Pool(numels, dtype, packed, gs).views, 0.3, out)
+        got.add(out.item())
+    assert len(got) == 1
+    # squares exact; at most N additions, each off by half a binary64 step of at most the total
+    assert abs(got.pop() - want) <= sum(numels) * 2.0 ** -53 * want
+
+
+@pytest.mark.parametrize("parts", [1, 2, 2047, 2048, 2049, 4097, 16383, 16384, 16385, 40000])
+def test_norm_s_partials(parts):
+    """One tile per partial, by count around where their sum changes its launches:
+    small whole numbers, whose squares add exactly."""
+    n = parts * 4096 - 5
+    x = torch.arange(n, device="cuda", dtype=torch.int32).remainder_(7).float()
+    lst = zs.GradTensors([x[:n // 2], x[n // 2:]] if parts == 2 else [x])
+    need = zs.grad_norm_sq_tensors_workspace_bytes(lst)
+    ws = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(1, dtype=torch.float64, device="cuda")
+    for _ in range(2):
+        zs.grad_norm_sq_tensors(lst, 1.0, out, ws[:need])
+        whole, rest = divmod(n, 7)
+        assert out.item() == whole * sum(k * k for k in range(7)) + sum(k * k for k in range(rest))
+    assert bool((ws[need:] == 0xA5).all())
