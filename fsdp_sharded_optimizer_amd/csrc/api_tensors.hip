@@ -402,7 +402,7 @@ extern "C" {
 int64_t grad_norm_sq_tensors_workspace_bytes(const zs_tensor* grads, int32_t count, int32_t grad_dtype) {
     const int64_t parts = norm_partials_of(grads, count, grad_dtype);
     if (parts < 0) return -1;
-    return (parts <= kListSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
+    return (parts <= kSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
 }
 
 int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad_dtype, double grad_scale,
