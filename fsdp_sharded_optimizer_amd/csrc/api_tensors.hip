@@ -126,8 +126,12 @@ public:
         return ZS_OK;
     }
     int32_t flush() {
-        if (count_ == 0) return ZS_OK;
+        if (tiles_ == 0) {   // nothing but tensors without elements
+            clear();
+            return ZS_OK;
+        }
         auto& tab = b_.tab;
+        tab.start[count_] = (uint32_t)tiles_;
         tab.shift = 0;
         while (((tiles_ - 1) >> tab.shift) >= kListBuckets) ++tab.shift;
         constexpr int kPer = Table::kPerWord;
@@ -270,27 +274,58 @@ int32_t step_tensors(const zs_adamw* hp, const zs_adamw_scalars* sc_dev, const z
 
 uint32_t q8_key(uint32_t seed, int64_t step) { return q8_mix(q8_mix(seed) + (uint32_t)step); }
 
-// the entries of one tensor's pieces: `a` and `b` advance by their element
-// sizes, `copy` by 2 bytes
+// The records of the tensors of a call, one after the other: `a` and `b` advance by
+// their element sizes, `copy` by 2 bytes.  numel 0: a record without tiles.
 template <typename Fill>
-int32_t add_q8(Q8Batch& batch, Fill& fill, void* state, int64_t numel, int32_t index, const void* a, int64_t asz,
-               const void* b, int64_t bsz, const void* copy) {
-    for (int64_t off = 0; off < numel; off += kLaunchElems) {
-        const int64_t n = launch_piece(numel, off);
-        int at = 0;
-        const int32_t rc = fill.add(ceil_div(n, kQ8Pad), at);
-        if (rc != ZS_OK) return rc;
-        const void* const ptr[4] = {advance(a, off * asz), advance(b, off * bsz), state, advance(copy, off * 2)};
-        Q8Entry& e = batch.e[at];
-        for (int j = 0; j < 4; ++j) e.lo[j] = ptr_lo(ptr[j]);
-        e.hi[0] = ptr_hi(ptr[0]) | ptr_hi(ptr[1]) << 16;
-        e.hi[1] = ptr_hi(ptr[2]) | ptr_hi(ptr[3]) << 16;
-        e.numel = (uint32_t)n;
-        e.index_off = (uint32_t)index | (uint32_t)(off / kLaunchElems) << 24;
-        e.padded = (uint32_t)(q8_padded(numel) / kQ8Pad);
+class Q8Records {
+public:
+    Q8Records(Q8Batch& b, Fill& fill) : b_(b), fill_(fill) {}
+    int32_t add(int32_t index, void* state, int64_t numel, const void* a, int64_t asz, const void* b, int64_t bsz,
+                const void* copy) {
+        const bool pieces = numel > kLaunchElems;
+        int64_t off = 0;
+        do {
+            const int64_t n = launch_piece(numel, off);
+            const void* const ptr[4] = {advance(a, off * asz), advance(b, off * bsz), state, advance(copy, off * 2)};
+            uint32_t top = 0, has = 0;
+            for (int j = 0; j < 4 && n > 0; ++j)
+                if (ptr[j] != nullptr) top |= (ptr_hi(ptr[j]) >> 8) << (8 * j), has |= 0xFFu << (8 * j);
+            // another window of addresses, or a piece before or after
+            if (pieces || b_.padded != 0 || ((b_.top ^ top) & has & known_) != 0) {
+                const int32_t rc = fill_.flush();
+                if (rc != ZS_OK) return rc;
+            }
+            int at = 0;
+            const int32_t rc = fill_.add(ceil_div(n, kQ8Pad), at);
+            if (rc != ZS_OK) return rc;
+            if (at == 0) {
+                known_ = b_.top = 0;
+                b_.index = (uint32_t)index;
+                b_.off = (uint32_t)(off / kLaunchElems);
+                b_.padded = pieces ? (uint32_t)(q8_padded(numel) / kQ8Pad) : 0;
+            }
+            b_.top |= top;
+            known_ |= has;
+            Q8Entry& e = b_.e[at];
+            e.hi = 0;
+            for (int j = 0; j < 4; ++j) {
+                e.lo[j] = ptr_lo(ptr[j]);
+                e.hi |= (ptr_hi(ptr[j]) & 0xFFu) << (8 * j);
+            }
+            const uint32_t tail = (uint32_t)(n > 0 ? (n - 1) % kQ8Pad : 0) | (a != nullptr ? kQ8Has0 : 0) |
+                                  (b != nullptr ? kQ8Has1 : 0) | (copy != nullptr ? kQ8Has3 : 0);
+            uint32_t& word = b_.tail[at / 2];
+            word = at % 2 == 0 ? tail : (word & 0xFFFFu) | tail << 16;
+            off += kLaunchElems;
+        } while (off < numel);
+        return ZS_OK;
     }
-    return ZS_OK;
-}
+
+private:
+    Q8Batch& b_;
+    Fill& fill_;
+    uint32_t known_ = 0;   // the bytes of b_.top that a record of this launch has set
+};
 
 int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_scalars* sc_dev,
                         const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
@@ -339,9 +374,10 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
         return launch_adamw_q8(x, param_dtype == ZS_BF16, grad_dtype == ZS_BF16, keep, tiles, as_stream(hip_stream));
     };
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
+    Q8Records<decltype(fill)> records(b, fill);
     for (int32_t k = 0; k < count; ++k) {
         const zs_adamw_q8_tensor& t = list[k];
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.param, psz, t.grad, gsz, t.param_bf16);
+        const int32_t rc = records.add(k, t.state_q8, t.numel, t.param, psz, t.grad, gsz, t.param_bf16);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();
@@ -377,10 +413,11 @@ int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool
                       : launch_q8_decode(x, dtype == ZS_BF16, tiles, as_stream(hip_stream));
     };
     Filler<Q8Batch, decltype(launch)> fill(b, launch);
+    Q8Records<decltype(fill)> records(b, fill);
     for (int32_t k = 0; k < count; ++k) {
         const zs_moments_q8& t = list[k];
-        if (!encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr) continue;
-        const int32_t rc = add_q8(b, fill, t.state_q8, t.numel, k, t.exp_avg, sz, t.exp_avg_sq, sz, nullptr);
+        const bool skip = !encode && t.exp_avg == nullptr && t.exp_avg_sq == nullptr;
+        const int32_t rc = records.add(k, t.state_q8, skip ? 0 : t.numel, t.exp_avg, sz, t.exp_avg_sq, sz, nullptr);
         if (rc != ZS_OK) return rc;
     }
     return fill.flush();

@@ -46,9 +46,8 @@ __global__ __launch_bounds__(kBlock) void norm_tensors_kernel(const NormBatch b,
     uint32_t first;
     const uint32_t t = find_tensor(b.tab, blockIdx.x, first);
     const NormEntry e = b.e[t];
-    const uint32_t next = min(b.tab.start[t + 1], gridDim.x);
     const T* const grad = unpack_ptr<const T>(e.lo, e.hi_tail) + (int64_t)(blockIdx.x - first) * kTile<BF16>;
-    const bool last = blockIdx.x + 1 == next;
+    const bool last = blockIdx.x + 1 == b.tab.start[t + 1];
     const int n = last ? (int)(e.hi_tail >> 16) + 1 : (int)kTile<BF16>;   // the tile's elements
     const int lane0 = threadIdx.x * VE;
     u32x4 v[kQ];

@@ -142,20 +142,10 @@ __device__ __forceinline__ uint32_t q8_encode4(const float (&x)[4], uint32_t e, 
     return (signs & 0x80808080u) | (out & 0x7F7F7F7Fu);
 }
 
-// Where a tensor's (entry's) codes and scales are.  Codes lie in chunks of
-// kQ8Pad = 512 elements, a chunk's exp_avg codes and then its exp_avg_sq codes:
-// the code of element 256 b + 4 l + j of a chunk (block b, lane l) is byte
-// 8 l + 4 b + j of either, so a lane's codes of both blocks are one access and
-// every stream of a wave is lane-contiguous.  (Both kinds in one run: the step
-// 0.3-1 % faster than in two arrays.)
-struct Q8At {
-    uint8_t* codes;
-    uint8_t* scales;   // two bytes per block: exp_avg's, exp_avg_sq's
-};
-__device__ __forceinline__ Q8At q8_at(const Q8Entry& e) {
-    uint8_t* const state = unpack_ptr<uint8_t>(e.lo[2], e.hi[1]);
-    const int64_t off = (int64_t)(e.index_off >> 24) * kLaunchElems, padded = (int64_t)e.padded * kQ8Pad;
-    return Q8At{state + 2 * off, state + 2 * padded + off / (kQ8Block / 2)};
-}
+// Codes lie in chunks of kQ8Pad = 512 elements, a chunk's exp_avg codes and then
+// its exp_avg_sq codes: the code of element 256 b + 4 l + j of a chunk (block b,
+// lane l) is byte 8 l + 4 b + j of either, so a lane's codes of both blocks are
+// one access and every stream of a wave is lane-contiguous.  (Both kinds in one
+// run: the step 0.3-1 % faster than in two arrays.)
 
 }  // namespace zs

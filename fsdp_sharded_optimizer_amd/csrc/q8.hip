@@ -38,27 +38,50 @@ constexpr unsigned kEncodeLds = 11264;   // of fp32 moments
 constexpr int64_t kCapElems = int64_t(1) << 25;
 unsigned cap(unsigned lds, int64_t elems) { return elems < kCapElems ? 0 : lds; }
 
-// Where a wave works: its tensor's entry and its chunk.
+// Where a wave works: its chunk of its tensor.
 struct Chunk {
     Q8Entry e;
-    int64_t first;     // of the entry, of the chunk's elements
-    int64_t i;         // of the lane's elements in the first block
+    uint32_t top, has;
+    int64_t entry;     // elements of the tensor's record before the chunk
+    uint64_t first;    // of the tensor before it
+    int n;             // elements in it
+    uint32_t index;    // the tensor's place in the caller's list
     uint8_t* codes;    // the lane's exp_avg codes
     uint8_t* scales;   // the chunk's
+
+    // the j-th pointer's elements of the chunk
+    template <typename T>
+    __device__ __forceinline__ T* at(int j) const {
+        return base<T>(j) + entry;
+    }
+    template <typename T>
+    __device__ __forceinline__ T* base(int j) const {
+        return unpack_ptr<T>(e.lo[j], (e.hi >> (8 * j) & 0xFFu) | (top >> (8 * j) & 0xFFu) << 8);
+    }
 };
 __device__ __forceinline__ Chunk chunk_of(const Q8Batch& b, bool runs) {
     const uint32_t w = runs ? tile_in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     uint32_t first_tile;
-    const Q8Entry e = b.e[find_tensor(b.tab, w, first_tile)];
-    const Q8At at = q8_at(e);
-    const int64_t first = (int64_t)(w - first_tile) * kQ8Pad;
-    return Chunk{e, first, first + threadIdx.x * 4, at.codes + 2 * first + threadIdx.x * (4 * kBlocks),
-                 at.scales + first / (kQ8Block / 2)};
+    const uint32_t t = find_tensor(b.tab, w, first_tile);
+    const uint32_t next = b.tab.start[t + 1], tail = b.tail[t / 2] >> (16 * (t % 2));
+    Chunk c;
+    c.e = b.e[t];
+    c.top = b.top;
+    c.has = tail;
+    c.entry = (int64_t)(w - first_tile) * kQ8Pad;
+    c.first = (uint64_t)b.off * kLaunchElems + (uint64_t)c.entry;
+    c.n = w + 1 == next ? (int)(tail & kQ8Tail) + 1 : (int)kQ8Pad;
+    c.index = b.index + t;
+    const int64_t padded = (int64_t)(b.padded != 0 ? b.padded : next - first_tile) * kQ8Pad;
+    uint8_t* const state = c.base<uint8_t>(2);
+    c.codes = state + 2 * c.first + threadIdx.x * (4 * kBlocks);
+    c.scales = state + 2 * padded + c.first / (kQ8Block / 2);
+    return c;
 }
 
 // 4 consecutive elements from i of n (zeros past the end).
 template <bool KEEP, typename T>
-__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool whole, float (&x)[4]) {
+__device__ __forceinline__ void load4(const T* p, int i, int n, bool whole, float (&x)[4]) {
     if (whole || i + 4 <= n) {
         const f32x4 w = ld4<KEEP>(p + i);
         x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
@@ -75,7 +98,7 @@ __device__ __forceinline__ void st4_hw(uint16_t* p, const f32x4& x) {
     __builtin_nontemporal_store(u32x2_any(w), reinterpret_cast<u32x2_any*>(p));
 }
 template <typename T>
-__device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, bool whole, const float (&x)[4]) {
+__device__ __forceinline__ void store4(T* p, int i, int n, bool whole, const float (&x)[4]) {
     if (whole || i + 4 <= n) {
         st4_hw(p + i, f32x4{x[0], x[1], x[2], x[3]});
     } else {
@@ -115,10 +138,9 @@ __device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, cons
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) most[2 * b] = max4(m[b]), most[2 * b + 1] = max4(v[b]);
     const uint32_t e = q8_scale(wave_max(most));
-    const uint32_t tensor_key = q8_mix(key + (c.e.index_off & 0xFFFFFFu) * kGolden);
+    const uint32_t tensor_key = q8_mix(key + c.index * kGolden);
     // the wave's first group; its groups share the upper 32 bits
-    const uint32_t group =
-        q8_group(((uint64_t)(c.e.index_off >> 24) * kLaunchElems + (uint64_t)c.first) / 4, tensor_key);
+    const uint32_t group = q8_group(c.first / 4, tensor_key);
     uint32_t mc[kBlocks], vc[kBlocks], scales = 0;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
@@ -161,19 +183,19 @@ template <bool PBF16, bool GBF16, bool WHOLE, bool FAST, bool KEEP, bool RUNS>
 __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc, const Chunk& c) {
     using P = typename GradType<PBF16>::T;
     using G = typename GradType<GBF16>::T;
-    const int64_t n = c.e.numel;
-    P* const param = unpack_ptr<P>(c.e.lo[0], c.e.hi[0]);
-    const G* const grad = unpack_ptr<const G>(c.e.lo[1], c.e.hi[0] >> 16);
-    uint16_t* const copy = unpack_ptr<uint16_t>(c.e.lo[3], c.e.hi[1] >> 16);
+    const int n = c.n, i = threadIdx.x * 4;
+    P* const param = c.at<P>(0);
+    const G* const grad = c.at<const G>(1);
+    uint16_t* const copy = c.at<uint16_t>(3);
     float g[kBlocks][4], p[kBlocks][4], m[kBlocks][4], v[kBlocks][4];
     uint32_t mc[kBlocks], vc[kBlocks];
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) load4<KEEP>(grad, c.i + k * kQ8Block, n, WHOLE, g[k]);
+    for (int k = 0; k < kBlocks; ++k) load4<KEEP>(grad, i + k * (int)kQ8Block, n, WHOLE, g[k]);
     load_codes(c.codes, mc);
     load_codes(c.codes + kQ8Pad, vc);
     uint32_t scales = load_scales(c.scales);
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) load4<RUNS>(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
+    for (int k = 0; k < kBlocks; ++k) load4<RUNS>(param, i + k * (int)kQ8Block, n, WHOLE, p[k]);
     float coef;
     if (!clip_coef(sc.adamw, b.norm_sq, coef)) return;
     scales = uniform(scales);
@@ -208,10 +230,10 @@ __device__ __forceinline__ void step_chunk(const Q8Batch& b, const Q8Scalars& sc
             v[k][j] = v_keep + v_new;
             p[k][j] = __builtin_fmaf(-adam_ratio<FAST>(a, inv_root, m[k][j], v[k][j]), a.step_size, p[k][j] * a.decay);
             // past the end: no part of the block's scale
-            if (!WHOLE && c.i + k * kQ8Block + j >= n) m[k][j] = v[k][j] = 0.0f;
+            if (!WHOLE && i + k * (int)kQ8Block + j >= n) m[k][j] = v[k][j] = 0.0f;
         }
-        store4(param, c.i + k * kQ8Block, n, WHOLE, p[k]);
-        if (!PBF16 && copy != nullptr) store4(copy, c.i + k * kQ8Block, n, WHOLE, p[k]);
+        store4(param, i + k * (int)kQ8Block, n, WHOLE, p[k]);
+        if (!PBF16 && (c.has & kQ8Has3)) store4(copy, i + k * (int)kQ8Block, n, WHOLE, p[k]);
     }
     store_moments(c, sc.key, m, v);
 }
@@ -220,7 +242,7 @@ template <bool PBF16, bool GBF16, bool DEV, bool KEEP, bool RUNS>
 __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
     const Chunk c = chunk_of(b, RUNS);
     const Q8Scalars sc = DEV ? *b.sc_dev : b.sc;
-    if (c.first + kQ8Pad <= (int64_t)c.e.numel && sc.adamw.eps >= kFastEps)
+    if (c.n == (int)kQ8Pad && sc.adamw.eps >= kFastEps)
         step_chunk<PBF16, GBF16, true, true, KEEP, RUNS>(b, sc, c);
     else
         step_chunk<PBF16, GBF16, false, false, KEEP, RUNS>(b, sc, c);
@@ -230,23 +252,21 @@ template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_encode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
     const Chunk c = chunk_of(b, false);
-    const int64_t n = c.e.numel;
-    const bool whole = c.first + kQ8Pad <= n;
-    const T* const from_m = unpack_ptr<const T>(c.e.lo[0], c.e.hi[0]);
-    const T* const from_v = unpack_ptr<const T>(c.e.lo[1], c.e.hi[0] >> 16);
+    const int n = c.n, i = threadIdx.x * 4;
+    const T* const from_m = c.at<const T>(0);
+    const T* const from_v = c.at<const T>(1);
     float m[kBlocks][4] = {}, v[kBlocks][4] = {};
-    if (whole && from_m != nullptr && from_v != nullptr) {   // no branch between the loads
+    if (n == (int)kQ8Pad && (c.has & kQ8Has0) && (c.has & kQ8Has1)) {   // no branch between the loads
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) {
-            load4<false>(from_m, c.i + k * kQ8Block, n, true, m[k]);
-            load4<false>(from_v, c.i + k * kQ8Block, n, true, v[k]);
+            load4<false>(from_m, i + k * (int)kQ8Block, n, true, m[k]);
+            load4<false>(from_v, i + k * (int)kQ8Block, n, true, v[k]);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) {
-            const int64_t i = c.i + k * kQ8Block;
-            if (from_m != nullptr) load4<false>(from_m, i, n, false, m[k]);
-            if (from_v != nullptr) load4<false>(from_v, i, n, false, v[k]);
+            if (c.has & kQ8Has0) load4<false>(from_m, i + k * (int)kQ8Block, n, false, m[k]);
+            if (c.has & kQ8Has1) load4<false>(from_v, i + k * (int)kQ8Block, n, false, v[k]);
         }
     }
 #pragma unroll
@@ -260,24 +280,24 @@ template <bool BF16>
 __global__ __launch_bounds__(kWave) void q8_decode_kernel(const Q8Batch b) {
     using T = typename GradType<BF16>::T;
     const Chunk c = chunk_of(b, b.runs != 0);
-    const int64_t n = c.e.numel;
-    const bool whole = c.first + kQ8Pad <= n;
+    const int n = c.n;
+    const bool whole = n == (int)kQ8Pad;
     uint32_t mc[kBlocks], vc[kBlocks];
     load_codes(c.codes, mc);
     load_codes(c.codes + kQ8Pad, vc);
     const uint32_t scales = uniform(load_scales(c.scales));
-    T* const m = unpack_ptr<T>(c.e.lo[0], c.e.hi[0]);
-    T* const v = unpack_ptr<T>(c.e.lo[1], c.e.hi[0] >> 16);
+    T* const m = c.at<T>(0);
+    T* const v = c.at<T>(1);
     wait_loads();
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
-        const int64_t i = c.i + k * kQ8Block;
+        const int i = threadIdx.x * 4 + k * (int)kQ8Block;
         float x[4];
-        if (m != nullptr) {
+        if (c.has & kQ8Has0) {
             q8_decode4<kTopM>(mc[k], scale_m(scales, k), x);
             store4(m, i, n, whole, x);
         }
-        if (v != nullptr) {
+        if (c.has & kQ8Has1) {
             q8_decode4<kTopV>(vc[k], scale_v(scales, k), x);
             store4(v, i, n, whole, x);
         }

@@ -6,14 +6,15 @@
 
 namespace zs {
 
-// One launch covers up to N tensors.  A tensor's elements are cut
-// in tiles; workgroups are laid out tensor after tensor, and start[t] is the
-// first workgroup of tensor t (kNoTile past the last).  A workgroup finds its
-// tensor in three dependent rounds of scalar loads: the tensor that a 32nd of
-// the launch begins in, the next 8 starts (again only where 8 small tensors
-// begin in one such part before the workgroup's), and the tensor's record.
-// Against a scan of every eighth start and then of 8, as the compiler
-// wrote them (through vector registers): the norm of 855M gradients 266 -> 250 us.
+// One launch covers up to N tensors.  A tensor's elements are cut in tiles;
+// workgroups are laid out tensor after tensor, and start[t] is the first
+// workgroup of tensor t (of the launch's end for the one past the last, then
+// kNoTile).  A workgroup finds its tensor in three dependent rounds of scalar
+// loads: the tensor that a 32nd of the launch begins in, the next 8 starts
+// (again only where 8 small tensors begin in one such part before the
+// workgroup's), and the tensor's record. Against a scan of every eighth start
+// and then of 8, as the compiler wrote them (through vector registers): the norm
+// of 855M gradients 266 -> 250 us.
 constexpr int kListBuckets = 32;
 constexpr int kListScan = 8;
 constexpr uint32_t kNoTile = 0xFFFFFFFFu;
@@ -65,8 +66,7 @@ __device__ __forceinline__ uint32_t tile_in_runs(uint32_t w, uint32_t n) {
 
 // A device address in 48 bits: its low word, and its upper 16 bits as one half
 // of a word.  A record of five pointers and a length is then 36 bytes, and the 4
-// KiB of kernel arguments hold 98 of them (the 291 tensors of a 7B model: 3
-// launches; with whole pointers 64, and 5 launches).
+// KiB of kernel arguments hold 98 of them (with whole pointers 64).
 template <typename T>
 __device__ __forceinline__ T* unpack_ptr(uint32_t lo, uint32_t hi16) {
     // global memory, said so: accesses through a pointer made from an integer
@@ -198,23 +198,30 @@ struct Q8Scalars {   // zs_adamw_q8_scalars
     uint32_t reserved;
 };
 
-// `off` elements of the tensor come before the entry's first, in units of
-// kLaunchElems; `padded` is the whole tensor's padded length in units of kQ8Pad;
-// the state is the whole tensor's buffer, the other pointers the entry's.  The
-// index is the tensor's place in the caller's list.
+// A record is 26 bytes with its tile start, so that the 291 tensors of a 7B
+// model are two launches (with whole pointers and lengths 98 to a launch, three:
+// 25M parameters in 290 tensors, step and read-out 78 -> 72 and 39 -> 35 us;
+// lists of a few long tensors 0-1 % slower).  Of an address the low word and
+// bits 32-39; bits 40-47 are the launch's (one window of 1 TiB for each stream;
+// another one starts another launch).  A tensor's tiles are whole but the last,
+// whose elements (less 1) are the tail.  Records are of consecutive tensors of
+// the caller's list, those without elements included (no tiles).  A piece of a
+// tensor longer than kLaunchElems is alone in its launch.
 constexpr int32_t kQ8MaxCount = 1 << 24;
 struct Q8Entry {
-    uint32_t lo[4];       // step: param, grad, state, bf16 re-cast (0: none);
-                          // conversions: exp_avg, exp_avg_sq (0: none), state
-    uint32_t hi[2];       // the first | the second << 16, state | re-cast << 16
-    uint32_t numel;
-    uint32_t index_off;   // index | off << 24
-    uint32_t padded;
+    uint32_t lo[4];       // step: param, grad, state, bf16 re-cast; conversions: exp_avg, exp_avg_sq, state
+    uint32_t hi;          // a byte of each
 };
+constexpr uint32_t kQ8Tail = 0x1FF, kQ8Has0 = 0x8000, kQ8Has1 = 0x4000, kQ8Has3 = 0x2000;   // which pointers are not NULL
 struct Q8Batch {
-    ListTable<98> tab;
-    uint32_t runs;        // not 0: workgroups take their tiles in runs (tile_in_runs)
-    Q8Entry e[98];
+    ListTable<150> tab;
+    Q8Entry e[150];
+    uint32_t tail[75];           // 16 bits each: the tail and kQ8Has bits
+    uint32_t runs;               // not 0: workgroups take their tiles in runs (tile_in_runs)
+    uint32_t top;                // bits 40-47 of the addresses, a byte of each
+    uint32_t index;              // the first record's place in the caller's list
+    uint32_t off, padded;        // a piece: elements before it in units of kLaunchElems, the whole tensor's padded
+                                 // length in units of kQ8Pad; otherwise 0
     const Q8Scalars* sc_dev;
     const double* norm_sq;       // nullable
     Q8Scalars sc;                // the conversions use the key alone

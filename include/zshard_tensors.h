@@ -7,9 +7,9 @@
  * norm over the list, the AdamW update of every tensor with its moments in
  * fp32 or in 8 bits, and the conversions of 8-bit moments.  The list is read
  * during the call only: tables of it travel in the kernel arguments (98
- * tensors to a launch, 328 for the norm), so nothing is allocated on the
- * device, copied to it or kept, and a call can be captured into a HIP graph as
- * is.
+ * tensors to a launch, 150 with 8-bit moments, 328 for the norm), so nothing is
+ * allocated on the device, copied to it or kept, and a call can be captured into
+ * a HIP graph as is.
  *
  * For every call: count >= 0 and the list not NULL with count > 0; a tensor's
  * numel >= 0, the sum at most 2^39; a tensor with numel 0 is skipped (its
