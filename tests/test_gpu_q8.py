@@ -348,3 +348,24 @@ def test_long_lists_off_cache_lines(pdtype):
         done.append((state, ps, ms, vs))
     for a, b in zip(*done):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("numels", [
+    [0] * 149 + [5, 600, 0, 7], [0] * 150 + [5, 600, 0, 7], [0] * 151 + [5], [3] + [0] * 400 + [513, 0, 0], [1] * 149 + [0, 0, 2],
+    [1] * 150 + [0, 300], [512] * 300, [0] * 320, [700, 0] * 160], ids=lambda n: f"{len(n)}-{sum(n)}")
+def test_empty_tensors_around_a_table(numels):
+    """Tensors without elements take a place in the list (the dither knows it),
+    also where a table ends; a step on them and a read-out of every second."""
+    pools, full, states, lst, p, g, m, v = make(numels, torch.float32, torch.bfloat16, True, 1, seed=61)
+    hp = zs.AdamWConfig(**HP, step=3)
+    zs.adamw_step_tensors_q8(hp, lst, seed=9)
+    check_step(numels, pools, states, p, g, m, v, hp, 9, np.float32(1.0))
+    assert guards_stand(full) and all(pool.guards_stand() for pool in pools.values())
+    out = Pool(numels, torch.float32, 1)
+    zs.moments_q8_decode(zs.Q8Moments(states, [x if k % 2 else None for k, x in enumerate(out.views)], None, numels))
+    assert out.guards_stand()
+    for k, x in enumerate(out.views):
+        if k % 2:
+            assert equal_values(x, m[k]), k
+        else:
+            assert bool((x == 7.75).all()), k
