@@ -331,7 +331,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
                         const zs_adamw_q8_tensor* list, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                         const double* norm_sq_dev, void* hip_stream) {
     const int64_t total = list_total(list, count);
-    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype) || count > kQ8MaxCount) return ZS_EINVAL;
+    if (total < 0 || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return ZS_EINVAL;
     if (sc_dev == nullptr) {
         const int32_t rc = adamw_check_hp(hp, total, norm_sq_dev);
         if (rc != ZS_OK) return rc;
@@ -387,7 +387,7 @@ int32_t step_tensors_q8(const zs_adamw* hp, uint32_t seed, const zs_adamw_q8_sca
 int32_t convert_q8(const zs_moments_q8* list, int32_t count, int32_t dtype, bool encode, uint32_t seed,
                    void* hip_stream) {
     const int64_t total = list_total(list, count);
-    if (total < 0 || !dtype_ok(dtype) || count > kQ8MaxCount) return ZS_EINVAL;
+    if (total < 0 || !dtype_ok(dtype)) return ZS_EINVAL;
     const int64_t sz = elem_size(dtype);
     Ranges ranges;
     OffLine off_line;

@@ -207,7 +207,6 @@ struct Q8Scalars {   // zs_adamw_q8_scalars
 // whose elements (less 1) are the tail.  Records are of consecutive tensors of
 // the caller's list, those without elements included (no tiles).  A piece of a
 // tensor longer than kLaunchElems is alone in its launch.
-constexpr int32_t kQ8MaxCount = 1 << 24;
 struct Q8Entry {
     uint32_t lo[4];       // step: param, grad, state, bf16 re-cast; conversions: exp_avg, exp_avg_sq, state
     uint32_t hi;          // a byte of each
