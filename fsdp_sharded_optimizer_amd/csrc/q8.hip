@@ -160,11 +160,10 @@ __device__ __forceinline__ void store_moments(const Chunk& c, uint32_t key, cons
 template <bool FAST>
 __device__ __forceinline__ float adam_ratio(const AdamwScalars& a, float inv_root, float m, float v) {
     if constexpr (FAST) {
-        // The hardware's square root and reciprocal are within 1 ulp: u is
-        // within 8 * 2^-24 of the exact quotient, far below the parameter's
-        // own rounding, for 11 issue slots against about 50 for IEEE division
-        // and root.  They flush subnormals: den is at least eps, and a
-        // subnormal v's root is below 2^-63.
+        // The hardware's square root and reciprocal are within 1 ulp (2^-23 of
+        // the value), the sum and the product half of one: u is within 8 * 2^-24
+        // of the exact quotient, far below the parameter's own rounding, for 11
+        // issue slots against about 50 for IEEE division and root.
         const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), inv_root, a.eps);
         return m * __builtin_amdgcn_rcpf(den);
     }
@@ -172,7 +171,17 @@ __device__ __forceinline__ float adam_ratio(const AdamwScalars& a, float inv_roo
     den = den + a.eps;
     return m / den;
 }
-constexpr float kFastEps = 0x1p-40f;
+// Whether adam_ratio<true>'s bound holds: the hardware's instructions flush
+// subnormals.  A subnormal v loses its root, below 2^-63: at most 2^-63 /
+// (bias_correction2_sqrt * eps) of den, which at 2^-40 and more is 2 * 2^-24, with
+// the 3 * 2^-24 of reciprocal and product under 8.  A den above 2^126 loses its
+// reciprocal, and all of it but eps is below 2^100 (a root up to 2^64, over a
+// correction of 2^-27 or more).  By the exponents alone, which are scalar
+// instructions: the product of two numbers is at least that of their powers of two.
+__device__ __forceinline__ bool fast_ratio(const AdamwScalars& a) {
+    const uint32_t eps = __float_as_uint(a.eps) >> 23, root = __float_as_uint(a.bias_correction2_sqrt) >> 23;
+    return eps + root >= 2 * 127 - 40 && eps < 127 + 100;
+}
 
 // One chunk's step.  WHOLE: all its elements are the tensor's.  KEEP: of the
 // gradients (keep_grads).  RUNS: the written streams lie off cache lines, tiles are
@@ -242,7 +251,7 @@ template <bool PBF16, bool GBF16, bool DEV, bool KEEP, bool RUNS>
 __global__ __launch_bounds__(kWave) void adamw_q8_kernel(const Q8Batch b) {
     const Chunk c = chunk_of(b, RUNS);
     const Q8Scalars sc = DEV ? *b.sc_dev : b.sc;
-    if (c.n == (int)kQ8Pad && sc.adamw.eps >= kFastEps)
+    if (c.n == (int)kQ8Pad && fast_ratio(sc.adamw))
         step_chunk<PBF16, GBF16, true, true, KEEP, RUNS>(b, sc, c);
     else
         step_chunk<PBF16, GBF16, false, false, KEEP, RUNS>(b, sc, c);

@@ -161,9 +161,10 @@ typedef struct {
  * adamw_step_tensors_q8 — adamw_step_tensors on 8-bit moments: each tensor's
  * moments are decoded, the new ones formed in fp32 as adamw_step forms them
  * (the same operations and roundings), the parameter updated with these, and
- * they are stored in 8 bits.  The parameter's step is formed with the
- * hardware's root and reciprocal where eps >= 2^-40, within 8 * 2^-24 of the
- * quotient of those moments.  The key is mix(mix(seed) + step), step the low
+ * they are stored in 8 bits.  The parameter's step is within 8 * 2^-24 of the
+ * quotient of those moments (formed with the hardware's root and reciprocal
+ * where eps times bias correction 2's root is at least 2^-38 and eps below 2^100,
+ * elsewhere and in a tensor's last, incomplete 512 elements with IEEE ones).  The key is mix(mix(seed) + step), step the low
  * 32 bits of hp->step: the same call on the same data gives the same bits.
  * A non-finite norm leaves every tensor and its moments unchanged; without a
  * norm a gradient that is not finite makes its whole block's moments NaN.

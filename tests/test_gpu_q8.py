@@ -369,3 +369,41 @@ def test_empty_tensors_around_a_table(numels):
             assert equal_values(x, m[k]), k
         else:
             assert bool((x == 7.75).all()), k
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.999, 0.999999])
+@pytest.mark.parametrize("eps", [2.0 ** -41, 2.0 ** -40, 1e-12, 2.0 ** -38, 2.0 ** -36, 2.0 ** -34, 2.0 ** -32, 2.0 ** -30, 1e-8])
+def test_the_update_s_bound_at_small_second_moments(eps, beta2):
+    """From a zero parameter, whose step is then all of it: second moments on
+    both sides of the least normal number, eps around where the form changes."""
+    print(eps, beta2, flush=True)
+    n = 4096
+    v = np.geomspace(2.0 ** -140, 2.0 ** -100, n)
+    sign = np.where(np.arange(n) % 3 == 0, -1.0, 1.0)
+    check_update_from_zero(sign * np.sqrt(v / (1 - beta2)), eps, beta2, lr=1e-3)
+
+
+@pytest.mark.parametrize("eps", [1.0, 2.0 ** 99, 2.0 ** 100, 2.0 ** 101, 2.0 ** 125, 2.0 ** 126, 2.0 ** 127, 3.4e38])
+def test_the_update_s_bound_at_large_eps(eps):
+    """eps up to the largest number, whose reciprocal is subnormal."""
+    print(eps, flush=True)
+    check_update_from_zero(np.geomspace(1e10, 1e18, 2048), eps, 0.999, lr=1e12)
+
+
+def check_update_from_zero(gradients, eps, beta2, lr):
+    """Steps 1 and 1000 from zero moments and parameters: the header's 8 * 2^-24
+    of the quotient, and half a step of the product with step_size, 2^-24."""
+    g = gradients.astype(np.float32)
+    n = g.size
+    zero = np.zeros(n, np.float32)
+    for step in (1, 1000):
+        hp = zs.AdamWConfig(lr=lr, beta1=0.9, beta2=beta2, eps=eps, step=step)
+        p = torch.zeros(n, device="cuda")
+        state = torch.zeros(zs.moments_q8_bytes(n), dtype=torch.uint8, device="cuda")
+        zs.adamw_step_tensors_q8(hp, zs.AdamWQ8Tensors([p], [from_np(g)], [state]))
+        s = zs.adamw_scalars(hp)
+        m, v = ref.new_moments(g, zero, zero, s, 1.0)
+        _, u = ref.update64(zero, m, v, s)
+        assert (np.abs(u) > 2.0 ** -100).all()
+        off = np.abs(p.cpu().double().numpy() + u) / np.abs(u) / E24
+        assert off.max() <= 8 + 1 + 2.0 ** -19, (step, off.max())     # their product's term of second order
