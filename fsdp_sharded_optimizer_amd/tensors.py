@@ -175,6 +175,8 @@ class _StepList(_List):
 
     def _take_grads(self, grads: "GradTensors", at: Sequence[int]) -> None:
         """The tensors `at` of a checked list of gradients."""
+        if grads.device != self.device and grads.count:   # it may have been marshalled while another GPU was current
+            raise ValueError(f"grads on {grads.device}, the list on {self.device}")
         at = np.fromiter(at, dtype=np.int64)
         if [grads.numels[k] for k in at] != self.numels:
             raise ValueError("grads: one per tensor of the list, of its size")

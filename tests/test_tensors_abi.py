@@ -280,3 +280,21 @@ def test_a_missing_library_is_an_error(monkeypatch, tmp_path):
     monkeypatch.setattr(B, "LIB_PATH", str(tmp_path / "libzshard.so"))
     with pytest.raises(RuntimeError):
         zs.moments_q8_bytes(5)
+
+
+def test_gradients_of_another_device_are_refused():
+    """Marshalled while another GPU was current: the check is of the lists'
+    devices, so descriptors without tensors behind them do."""
+    def of(cls, struct, index):
+        lst = object.__new__(cls)
+        T._List.__init__(lst, struct, [4, 0], torch.device("cuda", index))
+        return lst
+    for cls, struct in ((T.AdamWTensors, T.AdamWTensor), (T.AdamWQ8Tensors, T.AdamWQ8Tensor)):
+        lst, here, there = of(cls, struct, 0), of(T.GradTensors, B.Tensor, 0), of(T.GradTensors, B.Tensor, 1)
+        for k, g in enumerate((here, there)):
+            g._set("ptr", [None, None], [FAKE + k, 0])
+            g.grad_dtype = B.ZS_F32
+        lst.set_grads(here)
+        with pytest.raises(ValueError, match="cuda:1"):
+            lst.set_grads(there)
+        assert list(lst.array["grad"]) == [FAKE, 0]      # the refused ones changed nothing
