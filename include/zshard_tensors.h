@@ -105,7 +105,7 @@ ZS_API int32_t adamw_step_tensors_dev(const zs_adamw_scalars* scalars_dev, const
  * moment at beta2 = 0.999 would hardly ever change: one step moves it by
  * 0.1 %, half a code step is 3-6 %.)  A positive second moment never becomes
  * 0, so no update is divided by eps alone.  A block that holds a non-finite
- * value, or one of at least 1.875 * 2^127, has e = 255 and reads as NaN.
+ * value, or one above 1.875 * 2^127, has e = 255 and reads as NaN.
  * Dither, in 32-bit arithmetic: mix(x): x ^= x >> 16; x *= 0x6A09E667;
  * x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16.  A call has a key (below);
  * tensor k of the list key_k = mix(key + k * 0x9E3779B9); element i of it,

@@ -104,6 +104,27 @@ def test_conversion_edges():
     assert guards_stand(full)
 
 
+def test_the_largest_values():
+    """Blocks around 1.875 * 2^127, of either sign, that alone and beside small values."""
+    rows = []
+    for bits in (0x7F6FFFFF, 0x7F700000, 0x7F700001):
+        top = np.uint32(bits).view(np.float32)
+        row = np.linspace(0.25, 1, 300).astype(np.float32)
+        row[7] = -top
+        rows += [np.full(256, top), row]
+    numels = [r.size for r in rows]
+    full, states = states_of(numels)
+    zs.moments_q8_encode(zs.Q8Moments(states, [from_np(r) for r in rows], [from_np(np.abs(r)) for r in rows]), seed=3)
+    gm, gv = decoded(states, numels)
+    key = ref.key_of(3, 0)
+    for k, r in enumerate(rows):
+        assert equal_values(gm[k], ref.stored(r, "m", k, key)), k
+        assert equal_values(gv[k], ref.stored(np.abs(r), "v", k, key)), k
+        assert bool(torch.isnan(gm[k][:256]).all()) == (k >= 4) and not torch.isnan(gm[k][256:]).any()
+    assert bool((gm[2] == rows[2][0]).all()) and bool((gv[2] == rows[2][0]).all())      # kept as it is
+    assert guards_stand(full)
+
+
 def test_missing_moments_and_a_fresh_state():
     numels = [5, 1000]
     zero = [torch.zeros(zs.moments_q8_bytes(n), dtype=torch.uint8, device="cuda") for n in numels]

@@ -72,6 +72,15 @@ def test_edges(name):
             assert np.isfinite(y).all() and (np.abs(y - top) <= 0.25).all()
 
 
+@pytest.mark.parametrize("name", ["m", "v"])
+def test_the_largest_value(name):
+    """1.875 * 2^127 is the top code of the largest scale; anything above it makes its block NaN."""
+    top = np.uint32(0x7F700000)
+    for key in range(20):
+        assert (ref.stored(np.full(256, top.view(np.float32)), name, 0, key) == top.view(np.float32)).all()
+        assert np.isnan(ref.stored(np.full(256, (top + 1).view(np.float32)), name, 0, key)).all()
+
+
 def test_one_moment_moves_where_rounding_to_nearest_would_not():
     """beta2 = 0.999 and a squared gradient that falls to a quarter: the mean of
     the stored second moments follows the exact one.  Each store adds at most
