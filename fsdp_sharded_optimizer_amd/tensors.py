@@ -337,7 +337,7 @@ def moments_q8_encode(moments: Q8Moments, seed: int = 0, stream=None) -> None:
 
 def moments_q8_decode(moments: Q8Moments, stream=None) -> None:
     """The values of every tensor's 8-bit state into exp_avg and exp_avg_sq
-    (None: skipped); bf16 holds them exactly."""
+    (None: skipped); bf16 holds them exactly from 2^-130 up."""
     moments.check("moments_q8_decode")
     zs._check("moments_q8_decode", _lib().moments_q8_decode(
         moments.address, moments.count, moments.dtype, zs._stream(stream)))

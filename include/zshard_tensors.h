@@ -142,9 +142,8 @@ ZS_API int32_t moments_q8_encode(const zs_moments_q8* moments, int32_t count, in
 /*
  * moments_q8_decode — the values of 8-bit moments, for every tensor of a
  * list.  state_q8: read; exp_avg, exp_avg_sq: written, of dtype ZS_F32 or
- * ZS_BF16 (NULL: skipped).  A value has 4 significant bits, so bf16 holds it
- * exactly (fp32 and bf16 alike except below 2^-133, where bf16's subnormals
- * round it to nearest).
+ * ZS_BF16 (NULL: skipped).  A value has 4 significant bits, so fp32 holds it
+ * exactly, and bf16 from 2^-130 up (below, its subnormals round to nearest).
  */
 ZS_API int32_t moments_q8_decode(const zs_moments_q8* moments, int32_t count, int32_t dtype, void* hip_stream);
 

@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import fsdp_sharded_optimizer_amd as zs
 from tests import tensors_reference as ref
 from tests.parity import from_np, to_np
@@ -123,6 +124,30 @@ def test_the_largest_values():
         assert bool(torch.isnan(gm[k][:256]).all()) == (k >= 4) and not torch.isnan(gm[k][256:]).any()
     assert bool((gm[2] == rows[2][0]).all()) and bool((gv[2] == rows[2][0]).all())      # kept as it is
     assert guards_stand(full)
+
+
+def test_bf16_holds_the_values_from_2_to_the_minus_130():
+    """Read out into bf16: the values that fp32 holds, exactly from 2^-130 up and
+    to nearest below it (bf16's least step is 2^-133); stored again, the same."""
+    rng = np.random.default_rng(12)
+    rows = [(np.exp2(rng.uniform(lo, lo + 12, 512)) * (1 if lo % 2 else -1)).astype(np.float32)
+            for lo in (-149, -144, -138, -135, -132, -131, -130, -126)]
+    numels = [r.size for r in rows]
+    _, states = states_of(numels)
+    zs.moments_q8_encode(zs.Q8Moments(states, [from_np(r) for r in rows], [from_np(np.abs(r)) for r in rows]), seed=5)
+    wide, narrow = decoded(states, numels), decoded(states, numels, torch.bfloat16)
+    inexact = 0
+    for w, b in zip(wide[0] + wide[1], narrow[0] + narrow[1]):
+        w, b = w.cpu().numpy(), b.cpu().float().numpy()
+        assert np.array_equal(oracle.bf16_widen(oracle.bf16_rne(w)).view(np.uint32), b.view(np.uint32))
+        large = np.abs(w) >= 2.0 ** -130
+        assert np.array_equal(w[large], b[large])
+        inexact += int((w != b).sum())
+    assert inexact > 0
+    _, again = states_of(numels)
+    zs.moments_q8_encode(zs.Q8Moments(again, *narrow), seed=6)
+    for x, y in zip(narrow[0] + narrow[1], sum(decoded(again, numels, torch.bfloat16), [])):
+        assert same_bits(x, y)
 
 
 def test_missing_moments_and_a_fresh_state():
