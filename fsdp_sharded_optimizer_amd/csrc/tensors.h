@@ -28,13 +28,15 @@ struct ListTable {
 };
 
 // t + (w >= start) in two scalar instructions (the compiler takes the carry
-// through vector registers, about five times as long)
+// through vector registers, about five times as long).  The look-up and the order of
+// tiles are host functions too, for checks of the tables without a GPU.
 __device__ __forceinline__ void count_past(uint32_t& t, uint32_t w, uint32_t start) {
     asm("s_cmp_ge_u32 %1, %2\n\ts_addc_u32 %0, %0, 0" : "+s"(t) : "s"(w), "s"(start) : "scc");
 }
+__host__ inline void count_past(uint32_t& t, uint32_t w, uint32_t start) { t += w >= start; }
 
 template <int N>
-__device__ __forceinline__ uint32_t find_tensor(const ListTable<N>& tab, uint32_t w, uint32_t& first) {
+__host__ __device__ __forceinline__ uint32_t find_tensor(const ListTable<N>& tab, uint32_t w, uint32_t& first) {
     const uint32_t part = w >> tab.shift;
     constexpr uint32_t kPer = ListTable<N>::kPerWord, kBits = ListTable<N>::kBits;
     uint32_t t = tab.bucket[part / kPer] >> (kBits * (part % kPer)) & ((1u << kBits) - 1u), from;
@@ -58,7 +60,7 @@ __device__ __forceinline__ uint32_t find_tensor(const ListTable<N>& tab, uint32_
 // to odd offsets 507 -> 433 us, the 8-bit step 80 -> 76 at 25M fp32 parameters
 // (the same at 405M, whose parameters' lines are kept as well).  On aligned
 // tensors it costs 2-7 %.
-__device__ __forceinline__ uint32_t tile_in_runs(uint32_t w, uint32_t n) {
+__host__ __device__ __forceinline__ uint32_t tile_in_runs(uint32_t w, uint32_t n) {
     constexpr uint32_t kRun = 4, kAll = 8 * kRun;
     const uint32_t base = w / kAll * kAll, i = w % kAll;
     return base + kAll > n ? w : base + (i % 8) * kRun + i / 8;
