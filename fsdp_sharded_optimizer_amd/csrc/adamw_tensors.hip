@@ -19,13 +19,18 @@ namespace {
 constexpr int kWave = 64;
 // LDS reserved (never touched) per workgroup, to cap how many share a CU (too
 // many keep too many DRAM rows open): the cap that keeps about 80 KiB in flight
-// per CU.  Measured, % of the 8 TB/s peak at 8 / 10 / 12 / 13 / 14 / 16 KiB:
-// fp32 parameters with re-casts, fp32 gradients (634M) 77.1 / 77.1 / 79.1 / 80.6 /
-// 82.6 / 81.1, bf16 gradients (809M) 78.9 / 79.3 / 82.1 / 82.8 / 81.8 / 78.8; bf16
-// parameters, fp32 gradients (134M) 77 / 78 / 82 / 82 / 79, bf16 gradients (855M)
-// 81 / 82 / 81 / 78 / 74; uncapped 74-79.  A launch of less than 8M elements is
-// not long enough for that and ends sooner with more of it resident: 290
-// tensors of 25M bf16 parameters in five launches 107 us uncapped, 115 at 12 KiB.
+// per CU.  Measured, % of the 8 TB/s peak uncapped and at 8 / 10 / 12 / 13 / 14 / 16
+// KiB: fp32 parameters with re-casts, fp32 gradients (634M) 76.5, 79.9 / 80.7 /
+// 81.8 / 82.8 / 83.1 / 81.5, bf16 gradients (809M) 75.4, 79.2 / 79.9 / 81.1 / 82.7 /
+// 82.1 / 79.1; bf16 parameters, fp32 gradients (855M) 78.5, 81.3 / 81.2 / 82.2 /
+// 80.8 / 78.2 / 74.4, bf16 gradients (855M) 78.0, 81.1 / 81.5 / 80.6 / 77.9 / 74.3 /
+// 70.1.  A launch of less than 8M elements is not long enough for that: one tensor
+// of 2M / 8M / 32M / 64M elements, us uncapped and capped, fp32 parameters and
+// gradients 12.7, 13.6 / 40.6, 40.6 / 143, 142 / 318, 291; bf16 gradients 12.8,
+// 13.5 / 38.5, 36.8 / 139, 133 / 277, 263; bf16 parameters and gradients 10.8, 11.2 /
+// 30.0, 29.0 / 106, 102 / 208, 203.  (bf16 parameters with fp32 gradients are 4-7 %
+// faster uncapped up to 48M, 11.4, 11.6 / 33.1, 34.4 / 112, 118, and 4 % slower at
+// 64M, 241, 232.)
 template <bool PBF16, bool GBF16>
 constexpr unsigned kLds = PBF16 ? (GBF16 ? 10240 : 12288) : (GBF16 ? 13312 : 14336);
 // Where most tiles start off a cache line in some stream, their gradients are

@@ -439,6 +439,8 @@ extern "C" {
 int64_t grad_norm_sq_tensors_workspace_bytes(const zs_tensor* grads, int32_t count, int32_t grad_dtype) {
     const int64_t parts = norm_partials_of(grads, count, grad_dtype);
     if (parts < 0) return -1;
+    // only more than kListSumOneGroup partials use the stage; for fewer the size stays the one that programs
+    // have asked for so far
     return (parts <= kSumOneGroup ? parts : parts + kReduceChunks) * (int64_t)sizeof(double);
 }
 

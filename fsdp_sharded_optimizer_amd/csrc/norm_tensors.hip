@@ -2,10 +2,13 @@
 //
 // sum (double)fl32(widen(g) * scale)^2 over every tensor, in binary64: each
 // workgroup adds the squares of one tile of one tensor (zs::add_squares4, the
-// butterfly and LDS order of reduce.h) and writes one partial; the partials
-// are added by the fixed tree of launch_sum_partials.  The association depends
-// only on the numels, the dtype and their order.  HBM-bound: 4 (2) bytes per
-// element, read once.
+// butterfly and LDS order of reduce.h) and writes one partial.  A list of one
+// tile has its result then; up to kSumOneGroup = 2048 partials are added by one
+// 256-thread workgroup, more than kListSumOneGroup = 16384 by two launches with
+// a stage between them (both launch_sum_partials), those between by one
+// 1024-thread workgroup (list_sum_kernel).  The association depends only on the
+// numels, the dtype and their order.  HBM-bound: 4 (2) bytes per element, read
+// once.
 //
 // Layout: the standalone norm's (norm.hip): 256-thread workgroups, four
 // lane-contiguous 128-bit loads per lane (4096 fp32 or 8192 bf16 elements),

@@ -25,13 +25,18 @@ constexpr int kBlocks = (int)(kQ8Pad / kQ8Block);   // per chunk
 // CU, all it takes) / 6 / 7 / 8 / 9 / 11 / 12 KiB: the step on 809M fp32 parameters
 // (bf16 gradients, re-casts) 74.3 / 76.7 / 77.5 / 78.9 / 79.8 / 79.0 / 75.7; on 855M
 // bf16 parameters 79.7 / 80.7 / 81.4 / 79.5 / 77.4 / 73.3 / 67.1; reading 855M moments
-// out 80.2 / 80.9 / 78.1 / 74.2 / 69.1; storing 406M bf16 moments 83 / 83 / 80 / 73 / 68,
-// fp32 ones 77 / 78 / 79 / 80 / 82 / 83 / 78.  Tiles in runs, on 405M at odd offsets:
+// out 80.7 / 81.4 / 79.4 / 73.4 / 67.6 / 60.4 / 53.8; storing 406M bf16 moments 80.2 /
+// 77.6 / 75.1 / 71.5 / 67.6 / 61.4 / 54.8, fp32 ones 79.0 / 79.1 / 79.3 / 79.8 / 81.1 /
+// 81.4 / 77.2.  Tiles in runs, on 405M at odd offsets:
 // fp32 parameters 66 / 68 / 68 / 67 / 68 / 71 / 72 and 69 at 14, bf16 ones 74 / 76 / 75 / 71 /
 // 71 / 68 / 63, reading out 63 / 67 / 71 / 67 / 64 / 58 / 53.
 // (2 or 4 waves per workgroup: 0.5-4 points slower; plain instead of streaming
 // code accesses: the step 1 point slower.)  Launches of fewer than 2^25 elements
-// are not long enough for a cap to help.
+// are not long enough for a cap to help: one tensor of 8M / 16M / 32M / 64M, us
+// uncapped and capped, the step on bf16 parameters 16.6, 17.2 / 30.4, 30.7 / 53.2,
+// 54.0 / 99.3, 99.9, on fp32 ones 21.0, 21.8 / 38.6, 40.1 / 70.6, 72.2 / 135, 136,
+// reading out into bf16 14.0, 14.4 / 21.3, 21.0 / 36.0, 35.8 / 65.1, 63.2, storing
+// fp32 moments 15.7, 17.0 / 28.2, 29.7 / 53.6, 54.7 / 107, 101.
 template <bool PBF16, bool RUNS> constexpr unsigned kStepLds = PBF16 ? (RUNS ? 6144 : 7168) : (RUNS ? 12288 : 9216);
 constexpr unsigned kDecodeLds = 6144, kDecodeRunsLds = 7168;
 constexpr unsigned kEncodeLds = 11264;   // of fp32 moments
