@@ -5,7 +5,9 @@ C descriptors (GradTensors, AdamWTensors, AdamWQ8Tensors, Q8Moments), and
 passed to every call: a program's parameters and moments stay where they are
 from step to step, and a list of some hundred tensors costs more to marshal
 than to step.  Nothing is cached behind a call: a gradient that moved is given
-anew with ``set_grads``.
+anew with ``set_grads``.  A list holds its tensors, but cannot hold a storage
+that is replaced or resized under one (``t.data = ...``, ``resize_``): such a
+list is marshalled anew before its next call.
 """
 from __future__ import annotations
 
