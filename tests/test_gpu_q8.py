@@ -106,7 +106,7 @@ def test_conversion_edges():
 
 
 def test_the_largest_values():
-    """Blocks around 1.875 * 2^127, of either sign, that alone and beside small values."""
+    """Around 1.875 * 2^127: blocks of that value alone, and with it negative beside small ones."""
     rows = []
     for bits in (0x7F6FFFFF, 0x7F700000, 0x7F700001):
         top = np.uint32(bits).view(np.float32)
