@@ -40,6 +40,18 @@ Over lists of tensors (include/zshard_tensors.h), each list marshalled once:
     adamw_step_tensors(hp, tensors, norm_sq=None)               fp32 moments; _dev: scalars in device memory
     adamw_step_tensors_q8(hp, tensors, seed=0, norm_sq=None)    8-bit moments; _dev: q8_scalars_bytes(hp, seed)
     moments_q8_bytes(n) / moments_q8_encode(moments, seed=0) / moments_q8_decode(moments)
+    MixedTensors(tensors)                                       fp32 and bf16 tensors in one list
+    grad_norms_sq_tensors(grads, grad_scale, out, norms=None, workspace=None)   the norm of all, and of each
+    grad_clip_tensors(grads, out=None, grad_scale=1.0, max_norm=0.0, norm_sq=None)   scaled, clipped gradients
+
+Over lists of matrices (include/zshard_matrices.h):
+
+    ProductMatrices(a, b, d, c=None) / GramMatrices(a, d, c=None) / OrthogonalizeMatrices(inputs, outputs)
+    MuonMatrices(params, grads, momenta, param_bf16=None, scale="rms")
+    product_add_matrices(products, alpha=1.0, beta=1.0, workspace=None)         d = alpha op(a) op(b) + beta c
+    gram_add_matrices(grams, alpha=1.0, beta=1.0, workspace=None)               d = alpha a a^T + beta c
+    orthogonalize_matrices(matrices, steps=5, coefficients=..., eps=1e-7, workspace=None)
+    muon_step_matrices(hp, matrices, norm_sq=None, workspace=None)   _dev: muon_scalars_bytes(hp) in device memory
 
 TensorOptimizer(params, lr=..., state_bits=32 or 8) orders them, as
 ShardOptimizer does the calls over a flat shard.
@@ -95,6 +107,25 @@ from ._binding import (  # noqa: F401
     zero_shard_range,
 )
 from .arena import DeviceArena  # noqa: F401
+from .matrices import (  # noqa: F401
+    MATRIX_EXPORTS,
+    GramMatrices,
+    MuonConfig,
+    MuonMatrices,
+    OrthogonalizeMatrices,
+    ProductMatrices,
+    gram_add_matrices,
+    gram_add_matrices_workspace_bytes,
+    muon_scalars_bytes,
+    muon_step_matrices,
+    muon_step_matrices_dev,
+    muon_step_matrices_workspace_bytes,
+    orthogonalize_matrices,
+    orthogonalize_matrices_workspace_bytes,
+    product_add_matrices,
+    product_add_matrices_workspace_bytes,
+    update_scale,
+)
 from .step import ShardOptimizer  # noqa: F401
 from .tensor_step import TensorOptimizer  # noqa: F401
 from .tensors import (  # noqa: F401
@@ -104,13 +135,17 @@ from .tensors import (  # noqa: F401
     AdamWQ8Tensors,
     AdamWTensors,
     GradTensors,
+    MixedTensors,
     Q8Moments,
     adamw_step_tensors,
     adamw_step_tensors_dev,
     adamw_step_tensors_q8,
     adamw_step_tensors_q8_dev,
+    grad_clip_tensors,
     grad_norm_sq_tensors,
     grad_norm_sq_tensors_workspace_bytes,
+    grad_norms_sq_tensors,
+    grad_norms_sq_tensors_workspace_bytes,
     moments_q8_bytes,
     moments_q8_decode,
     moments_q8_encode,

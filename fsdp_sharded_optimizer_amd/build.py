@@ -39,11 +39,12 @@ def sources(sub: str = "csrc"):
     return sorted(glob.glob(os.path.join(HERE, sub, "*.hip")))
 
 
-# The calls over lists of tensors.  They are compiled into objects of their own
+# The calls over lists of tensors and matrices.  They are compiled into objects of their own
 # first: the compiler's id of a code object depends on how many sources share
 # its command, and the measured traffic of the flat step's kernels is recorded
 # under the digests of their code objects.
-OWN_OBJECTS = ("adamw_tensors.hip", "api_tensors.hip", "norm_tensors.hip", "q8.hip")
+OWN_OBJECTS = ("adamw_tensors.hip", "api_clip.hip", "api_matrices.hip", "api_tensors.hip", "clip.hip", "muon.hip",
+               "norm_tensors.hip", "products.hip", "q8.hip")
 
 
 def build(verbose: bool = False) -> str:

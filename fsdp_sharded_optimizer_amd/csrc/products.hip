@@ -1,0 +1,486 @@
+// Matrix products over lists: the caller's (alpha op(a) op(b) + beta c), and those
+// of the Newton-Schulz steps.
+#include "adamw_math.h"
+#include "matrices.h"
+#include "mfma_tile.h"
+
+namespace zs {
+namespace {
+
+using T256 = Tile<256, 256, 2, 4>;
+using T128 = Tile<128, 128, 2, 2>;
+using T64 = Tile<64, 64, 2, 2>;
+
+// The tile that workgroup w of a launch runs.  gfx950 deals workgroups to its 8
+// XCDs in turn: runs of as many consecutive tiles as an XCD works on at a time
+// go to one XCD, whose L2 then holds the rows and columns that they share.
+template <class T>
+__device__ __forceinline__ uint32_t tile_of(uint32_t w, uint32_t n) {
+    constexpr uint32_t kRun = T::BM == 256 ? 32 : T::BM == 128 ? 64 : 128, kAll = 8 * kRun;
+    const uint32_t base = w / kAll * kAll, i = w - base;
+    if (base + kAll <= n) return base + (i % 8) * kRun + i / 8;
+    return base + (uint32_t)xcd_slot(i, n - base);
+}
+
+// Tile t of a matrix of tm x tn tiles, as its row and column: bands of 4 rows.
+__device__ __forceinline__ void tile_in_bands(uint32_t t, uint32_t tm, uint32_t tn, uint32_t& i, uint32_t& j) {
+    constexpr uint32_t kBand = 4;
+    const uint32_t band = t / (kBand * tn), in = t - band * kBand * tn, h = min(kBand, tm - band * kBand);
+    i = band * kBand + in % h;
+    j = in / h;
+}
+// Tile t of a triangle: row i has i + 1 of them.
+__device__ __forceinline__ void tile_in_triangle(uint32_t t, uint32_t& i, uint32_t& j) {
+    uint32_t r = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > t) --r;
+    while ((r + 1) * (r + 2) / 2 <= t) ++r;
+    i = r;
+    j = t - r * (r + 1) / 2;
+}
+
+// Calls f(row, column, four consecutive columns' values) for a wave's part of a tile.
+template <class T, class F>
+__device__ __forceinline__ void for_each4(const f32x4 (&acc)[T::MI][T::NI], int m0, int n0, F&& f) {
+    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int row = m0 + (wave / T::WN) * (T::BM / T::WM) + (l & 15), col = n0 + (wave % T::WN) * (T::BN / T::WN) + (l >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) f(row + 16 * i, col + 16 * j, acc[i][j]);
+}
+
+template <class T>
+__device__ __forceinline__ Lds16* tile_lds() {
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * T::kStage];
+    return (Lds16*)lds;
+}
+
+// --- the caller's products ---------------------------------------------------
+
+// four values, or those before the row's end, at any element alignment
+__device__ __forceinline__ f32x4 load4(const void* p, int bf16, int64_t at, int left) {
+    float x[4] = {0, 0, 0, 0};
+    if (bf16) {
+        const uint16_t* const q = static_cast<const uint16_t*>(p) + at;
+        if (left >= 4) return ld4<true>(q);
+        for (int j = 0; j < left; ++j) x[j] = bf16_to_f32(q[j]);
+    } else {
+        const float* const q = static_cast<const float*>(p) + at;
+        if (left >= 4) return ld4<true>(q);
+        for (int j = 0; j < left; ++j) x[j] = q[j];
+    }
+    return f32x4{x[0], x[1], x[2], x[3]};
+}
+__device__ __forceinline__ void store4(float* p, const f32x4& x, int left) {
+    if (left >= 4) {
+        *reinterpret_cast<f32x4_any*>(p) = x;
+        return;
+    }
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    for (int j = 0; j < left; ++j) p[j] = v[j];
+}
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& x, int left) {
+    const uint32_t a = pack_bf16x2(x.x, x.y), b = pack_bf16x2(x.z, x.w);
+    if (left >= 4) {
+        *reinterpret_cast<u32x2_any*>(p) = u32x2{a, b};
+        return;
+    }
+    const uint32_t v[4] = {a, a >> 16, b, b >> 16};
+    for (int j = 0; j < left; ++j) p[j] = (uint16_t)v[j];
+}
+
+template <class T, bool BCOLS, bool SYM>
+__global__ __launch_bounds__(T::kThreads) void products_kernel(const ProductBatch b) {
+    uint32_t first;
+    const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
+    const ProductEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
+    uint32_t ti, tj;
+    if constexpr (SYM) tile_in_triangle(w - first, ti, tj);
+    else tile_in_bands(w - first, (e.m + T::BM - 1) / T::BM, (e.n + T::BN - 1) / T::BN, ti, tj);
+    const Operand a = {unpack_ptr<const uint16_t>(e.lo[0], e.hi[0]), (int64_t)e.lda, (int)e.m};
+    const Operand o = {unpack_ptr<const uint16_t>(e.lo[1], e.hi[0] >> 16), (int64_t)e.ldb, BCOLS ? (int)e.ldb : (int)e.n};
+    const void* const c = unpack_ptr<const uint16_t>(e.lo[2], e.hi[1]);
+    void* const d = unpack_ptr<uint16_t>(e.lo[3], e.hi[1] >> 16);
+    const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN, m = (int)e.m, n = (int)e.n;
+    f32x4 acc[T::MI][T::NI];
+    multiply<T, true, BCOLS>(a, o, m0, n0, (int)e.k_tiles, tile_lds<T>(), acc);
+    const float alpha = b.alpha, beta = b.beta;
+    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 x) {
+        if (r >= m || q >= n) return;
+        const int64_t at = (int64_t)r * n + q;
+        const int left = n - q;
+        x *= alpha;
+        if (c != nullptr) x += load4(c, b.c_bf16, at, left) * beta;
+        if (!SYM || ti != tj) {
+            if (b.d_bf16) store4(static_cast<uint16_t*>(d) + at, x, left);
+            else store4(static_cast<float*>(d) + at, x, left);
+        }
+        if constexpr (SYM) {
+            // the mirror; of a diagonal tile both triangles from the lower one (the three
+            // products of split values are not formed in the same order above it)
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= left || q + j > r) continue;
+                const int64_t mirror = (int64_t)(q + j) * n + r;
+                if (b.d_bf16) {
+                    const uint16_t y = (uint16_t)f32_to_bf16_rne(v[j]);
+                    if (ti == tj) static_cast<uint16_t*>(d)[at + j] = y;
+                    static_cast<uint16_t*>(d)[mirror] = y;
+                } else {
+                    if (ti == tj) static_cast<float*>(d)[at + j] = v[j];
+                    static_cast<float*>(d)[mirror] = v[j];
+                }
+            }
+        }
+    });
+}
+
+// --- the Newton-Schulz steps ---------------------------------------------------
+
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 widen4(const f16x4& x) { return f32x4{(float)x.x, (float)x.y, (float)x.z, (float)x.w}; }
+__device__ __forceinline__ f16x4 narrow4(const f32x4& x) {
+    return f16x4{(_Float16)x.x, (_Float16)x.y, (_Float16)x.z, (_Float16)x.w};
+}
+
+// S = X X^T, or b S + c S S: symmetric, tiles above the diagonal mirrored.
+template <class T, bool POLY>
+__global__ __launch_bounds__(T::kThreads) void ns_square_kernel(const NsBatch b) {
+    uint32_t first, ti, tj;
+    const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
+    const NsEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
+    tile_in_triangle(w - first, ti, tj);
+    const NsPlace p(e.m, e.n);
+    char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN, mp = (int)p.mp;
+    const int k = POLY ? mp : (int)p.np;
+    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base + (POLY ? p.s() : p.hi(b.which)));
+    const Operand o = {x, k, mp};
+    f32x4 acc[T::MI][T::NI];
+    multiply<T, false, false>(o, o, m0, n0, k / kTileK, tile_lds<T>(), acc);
+    const float cb = b.sc_dev ? b.sc_dev->b : b.b, cc = (b.sc_dev ? b.sc_dev->c : b.c) * (1.0f / kNsScale);
+    const _Float16* const s = reinterpret_cast<const _Float16*>(base + p.s());
+    _Float16* const out = reinterpret_cast<_Float16*>(base + (POLY ? p.poly() : p.s()));
+    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 v) {
+        if (r >= mp || q >= mp) return;
+        const int64_t at = (int64_t)r * mp + q;
+        if constexpr (POLY) v = widen4(*reinterpret_cast<const f16x4*>(s + at)) * cb + v * cc;
+        else v *= 1.0f / kNsScale;
+        const f16x4 h = narrow4(v);
+        *reinterpret_cast<f16x4*>(out + at) = h;
+        if (ti != tj) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[(int64_t)(q + j) * mp + r] = h[j];
+        }
+    });
+}
+
+// a X + P X (P = b S + c S^2), X's pair as the residual
+template <class T, class F>
+__device__ __forceinline__ void ns_update(const char* base, const NsPlace& p, int which, float a, int m0, int n0, F&& f) {
+    const int mp = (int)p.mp, np = (int)p.np;
+    const Operand poly = {reinterpret_cast<const uint16_t*>(base + p.poly()), mp, mp};
+    const Operand x = {reinterpret_cast<const uint16_t*>(base + p.hi(which)), np, np};
+    f32x4 acc[T::MI][T::NI];
+    multiply<T, false, true>(poly, x, m0, n0, mp / kTileK, tile_lds<T>(), acc);
+    const _Float16* const hi = reinterpret_cast<const _Float16*>(base + p.hi(which));
+    const _Float16* const lo = reinterpret_cast<const _Float16*>(base + p.lo(which));
+    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 v) {
+        if (r >= mp || q >= np) return;
+        const int64_t at = (int64_t)r * np + q;
+        const f32x4 res = widen4(*reinterpret_cast<const f16x4*>(hi + at)) + widen4(*reinterpret_cast<const f16x4*>(lo + at)) * (1.0f / kNsLow);
+        f(r, q, at, res * a + v * (1.0f / kNsScale));
+    });
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void ns_update_kernel(const NsBatch b) {
+    uint32_t first, ti, tj;
+    const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
+    const NsEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
+    const NsPlace p(e.m, e.n);
+    tile_in_bands(w - first, (uint32_t)((p.mp + T::BM - 1) / T::BM), (uint32_t)((p.np + T::BN - 1) / T::BN), ti, tj);
+    char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    _Float16* const hi = reinterpret_cast<_Float16*>(base + p.hi(1 - b.which));
+    _Float16* const lo = reinterpret_cast<_Float16*>(base + p.lo(1 - b.which));
+    ns_update<T>(base, p, b.which, b.sc_dev ? b.sc_dev->a : b.a, (int)ti * T::BM, (int)tj * T::BN,
+                 [&](int, int, int64_t at, f32x4 v) {
+                     f16x4 h, l;
+#pragma unroll
+                     for (int j = 0; j < 4; ++j) {
+                         _Float16 x, y;
+                         split_f16(v[j], x, y);
+                         h[j] = x;
+                         l[j] = y;
+                     }
+                     *reinterpret_cast<f16x4*>(hi + at) = h;
+                     *reinterpret_cast<f16x4*>(lo + at) = l;
+                 });
+}
+
+// The epilogue of the last step: four values v of X's row r from column q on, still
+// times kNsScale, to their destination.
+template <int KIND>
+struct Destination {
+    using P = typename GradType<KIND != kFinalParamF32>::T;
+    P* param;
+    uint16_t* copy;
+    int m, n;
+    bool tall;
+    float decay, step;
+    __device__ __forceinline__ Destination(const FinalEntry& e, const MuonScalars& sc)
+        : param(unpack_ptr<P>(e.lo[0], e.hi)), copy(unpack_ptr<uint16_t>(e.lo[1], e.hi >> 16)), m((int)e.m),
+          n((int)(e.n & ~kTall)), tall((e.n & kTall) != 0), decay(sc.decay), step(sc.lr * e.scale) {}
+    __device__ __forceinline__ void put(int r, int q, f32x4 v) const {
+        if (r >= m || q >= n) return;
+        const int left = n - q;
+        if (!tall) {
+            const int64_t at = (int64_t)r * n + q;
+            if constexpr (KIND != kFinalBf16) v = load4(param, KIND == kFinalParamBf16, at, left) * decay - v * step;
+            store4(param + at, v, left);
+            if (KIND == kFinalParamF32 && copy != nullptr) store4(copy + at, v, left);
+            return;
+        }
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= left) break;
+            const int64_t at = (int64_t)(q + j) * m + r;
+            float y = x[j];
+            if constexpr (KIND != kFinalBf16) y = widen(param[at]) * decay - y * step;
+            st1(param + at, y);
+            if (KIND == kFinalParamF32 && copy != nullptr) st1(copy + at, y);
+        }
+    }
+};
+
+// A norm that is not finite: no step.
+template <int KIND>
+__device__ __forceinline__ bool skipped(const FinalBatch& b, const MuonScalars& sc) {
+    if constexpr (KIND == kFinalBf16) return false;
+    return b.norm_sq != nullptr && !__builtin_isfinite(*b.norm_sq + sc.extra_norm_sq);
+}
+
+template <class T, int KIND>
+__global__ __launch_bounds__(T::kThreads) void ns_final_kernel(const FinalBatch b) {
+    uint32_t first, ti, tj;
+    const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
+    const FinalEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
+    const MuonScalars& sc = b.sc_dev ? *b.sc_dev : b.sc;
+    if (skipped<KIND>(b, sc)) return;
+    const Destination<KIND> to(e, sc);
+    const NsPlace p(to.m, to.n);
+    tile_in_bands(w - first, (uint32_t)((to.m + T::BM - 1) / T::BM), (uint32_t)((to.n + T::BN - 1) / T::BN), ti, tj);
+    ns_update<T>(b.ws + (int64_t)e.base * kNsUnit, p, b.which, sc.a, (int)ti * T::BM, (int)tj * T::BN,
+                 [&](int r, int q, int64_t, f32x4 v) { to.put(r, q, v * (1.0f / kNsScale)); });
+}
+
+// --- matrices whose short side is at most 64 -------------------------------------
+
+// One partial sum of S from the pairs: hi hi^T + hi lo^T + lo hi^T (the fourth
+// product is below fp32's last bit).
+__global__ __launch_bounds__(T64::kThreads) void skinny_gram_kernel(const NsBatch b) {
+    uint32_t first;
+    const NsEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
+    const SkinnyPlace p(e.n);
+    char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    const int64_t chunk = blockIdx.x - first, from = chunk * p.chunk, left = p.np / kTileK - from;
+    const int tiles = (int)(left < p.chunk ? left : p.chunk);
+    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base) + from * kTileK;
+    const Operand hi = {x, p.np, (int)kSkinny}, lo = {x + p.x / 2, p.np, (int)kSkinny};
+    f32x4 sum[T64::MI][T64::NI], acc[T64::MI][T64::NI];
+    multiply<T64, false, false>(hi, lo, 0, 0, tiles, tile_lds<T64>(), sum);
+    multiply<T64, false, false>(lo, hi, 0, 0, tiles, tile_lds<T64>(), acc);
+#pragma unroll
+    for (int i = 0; i < T64::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T64::NI; ++j) sum[i][j] = (sum[i][j] + acc[i][j]) * (1.0f / kNsLow);
+    multiply<T64, false, false>(hi, hi, 0, 0, tiles, tile_lds<T64>(), acc);
+    float* const out = reinterpret_cast<float*>(base + p.parts() + chunk * SkinnyPlace::kPart);
+#pragma unroll
+    for (int i = 0; i < T64::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T64::NI; ++j) acc[i][j] += sum[i][j];
+    for_each4<T64>(acc, 0, 0, [&](int r, int q, f32x4 v) { *reinterpret_cast<f32x4*>(out + r * kSkinny + q) = v; });
+}
+
+// 64 x 64 matrices in LDS, rows of 65 words.
+constexpr int kPitch = 65;
+struct Square {
+    float v[kSkinny * kPitch];
+};
+
+// f(row, column, value) of x y: wave w forms rows 16 w ... with the fp32 matrix
+// instruction (lane l: row l % 16 of a and column l % 16 of b at k = l / 16).
+template <class F>
+__device__ __forceinline__ void square_product(const Square& x, const Square& y, F&& f) {
+    const int l = threadIdx.x & 63, row = (threadIdx.x >> 6) * 16, at = l & 15, kl = l >> 4;
+    f32x4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll 4
+    for (int k = 0; k < kSkinny; k += 4) {
+        const float a = x.v[(row + at) * kPitch + k + kl];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, y.v[(k + kl) * kPitch + 16 * j + at], acc[j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f(row + 4 * kl + i, 16 * j + at, acc[j][i]);
+}
+
+// Q = M_1 M_2 ... with M = a I + b S + c S^2 and S <- M S M after each (all
+// polynomials of the first S: they commute), and Q as two fp16 values times a power
+// of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].
+__global__ __launch_bounds__(T64::kThreads) void skinny_steps_kernel(const NsBatch b) {
+    __shared__ Square s, t, m, q;
+    const NsEntry e = b.e[blockIdx.x];
+    const SkinnyPlace p(e.n);
+    char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    const float ca = b.sc_dev ? b.sc_dev->a : b.a, cb = b.sc_dev ? b.sc_dev->b : b.b, cc = b.sc_dev ? b.sc_dev->c : b.c;
+    const float* const parts = reinterpret_cast<const float*>(base + p.parts());
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads) {
+        float x = 0.0f;
+        for (int64_t k = 0; k < p.chunks; ++k) x += parts[k * (kSkinny * kSkinny) + i];
+        s.v[i / kSkinny * kPitch + i % kSkinny] = x * (1.0f / (kNsScale * kNsScale));
+    }
+    __syncthreads();
+    for (int step = 0; step < b.steps; ++step) {
+        square_product(s, s, [&](int r, int c, float x) {
+            const int at = r * kPitch + c;
+            m.v[at] = (s.v[at] * cb + x * cc) + (r == c ? ca : 0.0f);
+            if (step == 0) q.v[at] = m.v[at];
+        });
+        __syncthreads();
+        const bool more = step + 1 < b.steps;
+        float kept[16];   // what a product of q or s by itself would overwrite
+        if (step > 0) {
+            int n = 0;
+            square_product(m, q, [&](int, int, float x) { kept[n++] = x; });
+            __syncthreads();
+            n = 0;
+            const int l = threadIdx.x & 63, row = (threadIdx.x >> 6) * 16 + 4 * (l >> 4), col = l & 15;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q.v[(row + i) * kPitch + 16 * j + col] = kept[n++];
+        }
+        if (more) {
+            square_product(m, s, [&](int r, int c, float x) { t.v[r * kPitch + c] = x; });
+            __syncthreads();
+            square_product(t, m, [&](int r, int c, float x) { s.v[r * kPitch + c] = x; });
+        }
+        __syncthreads();
+    }
+    // the scale: Q's largest magnitude to [2^12, 2^13)
+    float most = 0.0f;
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads)
+        most = fmaxf(most, fabsf(q.v[i / kSkinny * kPitch + i % kSkinny]));
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) t.v[threadIdx.x >> 6] = most;
+    __syncthreads();
+    most = fmaxf(fmaxf(t.v[0], t.v[1]), fmaxf(t.v[2], t.v[3]));
+    int exponent = 0;
+    if (most > 0.0f && __builtin_isfinite(most)) (void)frexpf(most, &exponent);
+    const float scale = ldexpf(1.0f, 13 - exponent);
+    _Float16* const out = reinterpret_cast<_Float16*>(base + p.q());
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads) {
+        const int r = i / (int)kSkinny, c = i % (int)kSkinny;
+        const float x = q.v[r * kPitch + c] * scale;
+        _Float16 h, l;
+        split_f16(x, h, l);
+        out[r * 3 * kSkinny + c] = h;
+        out[r * 3 * kSkinny + kSkinny + c] = (_Float16)((float)h * (1.0f / kNsLow));
+        out[r * 3 * kSkinny + 2 * kSkinny + c] = (_Float16)((float)l * (1.0f / kNsLow));
+    }
+    if (threadIdx.x == 0) *reinterpret_cast<float*>(base + p.scale()) = ldexpf(1.0f / kNsScale, exponent - 13);
+}
+
+template <int KIND>
+__global__ __launch_bounds__(T64::kThreads) void skinny_final_kernel(const FinalBatch b) {
+    uint32_t first;
+    const FinalEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
+    const MuonScalars& sc = b.sc_dev ? *b.sc_dev : b.sc;
+    if (skipped<KIND>(b, sc)) return;
+    const Destination<KIND> to(e, sc);
+    const SkinnyPlace p(to.n);
+    const char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    const int n0 = (int)(blockIdx.x - first) * T64::BN;
+    const Operand q = {reinterpret_cast<const uint16_t*>(base + p.q()), 3 * kSkinny, (int)kSkinny};
+    const Operand x = {reinterpret_cast<const uint16_t*>(base), p.np, (int)p.np};
+    f32x4 acc[T64::MI][T64::NI];
+    multiply<T64, false, true>(q, x, 0, n0, 3, tile_lds<T64>(), acc);
+    const float scale = *reinterpret_cast<const float*>(base + p.scale());
+    for_each4<T64>(acc, 0, n0, [&](int r, int c, f32x4 v) { to.put(r, c, v * scale); });
+}
+
+template <class T>
+void launch_products_of(const ProductBatch& b, bool b_cols, bool sym, unsigned tiles, hipStream_t stream) {
+    const dim3 grid(tiles), block(T::kThreads);
+    if (sym) hipLaunchKernelGGL((products_kernel<T, false, true>), grid, block, 0, stream, b);
+    else if (b_cols) hipLaunchKernelGGL((products_kernel<T, true, false>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((products_kernel<T, false, false>), grid, block, 0, stream, b);
+}
+
+template <class T>
+void launch_ns_of(const NsBatch& b, int phase, unsigned tiles, hipStream_t stream) {
+    const dim3 grid(tiles), block(T::kThreads);
+    if (phase == kNsGram) hipLaunchKernelGGL((ns_square_kernel<T, false>), grid, block, 0, stream, b);
+    else if (phase == kNsPoly) hipLaunchKernelGGL((ns_square_kernel<T, true>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((ns_update_kernel<T>), grid, block, 0, stream, b);
+}
+
+template <class T>
+void launch_final_of(const FinalBatch& b, int kind, unsigned tiles, hipStream_t stream) {
+    const dim3 grid(tiles), block(T::kThreads);
+    if (kind == kFinalBf16) hipLaunchKernelGGL((ns_final_kernel<T, kFinalBf16>), grid, block, 0, stream, b);
+    else if (kind == kFinalParamF32) hipLaunchKernelGGL((ns_final_kernel<T, kFinalParamF32>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((ns_final_kernel<T, kFinalParamBf16>), grid, block, 0, stream, b);
+}
+
+}  // namespace
+
+hipError_t launch_products(const ProductBatch& b, int size, bool b_cols, bool sym, int64_t tiles, hipStream_t stream) {
+    if (size == kTile256) launch_products_of<T256>(b, b_cols, sym, (unsigned)tiles, stream);
+    else if (size == kTile128) launch_products_of<T128>(b, b_cols, sym, (unsigned)tiles, stream);
+    else launch_products_of<T64>(b, b_cols, sym, (unsigned)tiles, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_ns(const NsBatch& b, int phase, int size, int64_t tiles, hipStream_t stream) {
+    if (size == kTile256) launch_ns_of<T256>(b, phase, (unsigned)tiles, stream);
+    else if (size == kTile128) launch_ns_of<T128>(b, phase, (unsigned)tiles, stream);
+    else launch_ns_of<T64>(b, phase, (unsigned)tiles, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_skinny_gram(const NsBatch& b, int64_t tiles, hipStream_t stream) {
+    hipLaunchKernelGGL(skinny_gram_kernel, dim3((unsigned)tiles), dim3(T64::kThreads), 0, stream, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_skinny_steps(const NsBatch& b, int64_t count, hipStream_t stream) {
+    hipLaunchKernelGGL(skinny_steps_kernel, dim3((unsigned)count), dim3(T64::kThreads), 0, stream, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_ns_final(const FinalBatch& b, int kind, int size, bool skinny, int64_t tiles, hipStream_t stream) {
+    if (skinny) {
+        const dim3 grid((unsigned)tiles), block(T64::kThreads);
+        if (kind == kFinalBf16) hipLaunchKernelGGL((skinny_final_kernel<kFinalBf16>), grid, block, 0, stream, b);
+        else if (kind == kFinalParamF32) hipLaunchKernelGGL((skinny_final_kernel<kFinalParamF32>), grid, block, 0, stream, b);
+        else hipLaunchKernelGGL((skinny_final_kernel<kFinalParamBf16>), grid, block, 0, stream, b);
+        return hipGetLastError();
+    }
+    if (size == kTile256) launch_final_of<T256>(b, kind, (unsigned)tiles, stream);
+    else if (size == kTile128) launch_final_of<T128>(b, kind, (unsigned)tiles, stream);
+    else launch_final_of<T64>(b, kind, (unsigned)tiles, stream);
+    return hipGetLastError();
+}
+
+}  // namespace zs

@@ -1,7 +1,7 @@
 """ctypes binding of the calls over lists of tensors (include/zshard_tensors.h).
 
 A list is marshalled once, into an object that holds its tensors and their
-C descriptors (GradTensors, AdamWTensors, AdamWQ8Tensors, Q8Moments), and
+C descriptors (GradTensors, MixedTensors, AdamWTensors, AdamWQ8Tensors, Q8Moments), and
 passed to every call: a program's parameters and moments stay where they are
 from step to step, and a list of some hundred tensors costs more to marshal
 than to step.  Nothing is cached behind a call: a gradient that moved is given
@@ -25,7 +25,7 @@ Q8_BLOCK = 256   # ZS_Q8_BLOCK: elements that share a scale
 TENSOR_EXPORTS = (
     "grad_norm_sq_tensors_workspace_bytes", "grad_norm_sq_tensors", "adamw_step_tensors", "adamw_step_tensors_dev",
     "moments_q8_bytes", "moments_q8_encode", "moments_q8_decode", "adamw_step_tensors_q8", "adamw_q8_scalars",
-    "adamw_step_tensors_q8_dev",
+    "adamw_step_tensors_q8_dev", "grad_norms_sq_tensors_workspace_bytes", "grad_norms_sq_tensors", "grad_clip_tensors",
 )
 
 
@@ -37,6 +37,12 @@ def _struct(name: str, pointers: Sequence[str]):
 AdamWTensor = _struct("AdamWTensor", ("param", "grad", "exp_avg", "exp_avg_sq", "param_bf16"))
 AdamWQ8Tensor = _struct("AdamWQ8Tensor", ("param", "grad", "state_q8", "param_bf16"))
 MomentsQ8 = _struct("MomentsQ8", ("exp_avg", "exp_avg_sq", "state_q8"))
+
+
+class MixedTensor(ctypes.Structure):
+    """zs_mixed_tensor"""
+    _fields_ = [("ptr", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class AdamWQ8Scalars(ctypes.Structure):
@@ -63,7 +69,10 @@ def _lib() -> ctypes.CDLL:
                 ("moments_q8_decode", [P, I32, I32, P], I32),
                 ("adamw_step_tensors_q8", [HP, U32, P, I32, I32, I32, P, P], I32),
                 ("adamw_q8_scalars", [HP, U32, ctypes.POINTER(AdamWQ8Scalars)], I32),
-                ("adamw_step_tensors_q8_dev", [P, P, I32, I32, I32, P, P], I32)):
+                ("adamw_step_tensors_q8_dev", [P, P, I32, I32, I32, P, P], I32),
+                ("grad_norms_sq_tensors_workspace_bytes", [P, I32], I64),
+                ("grad_norms_sq_tensors", [P, I32, D, P, P, P, I64, P], I32),
+                ("grad_clip_tensors", [P, P, I32, D, D, D, P, P], I32)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
         _ready = L
@@ -74,9 +83,10 @@ def _lib() -> ctypes.CDLL:
 # lists
 # ---------------------------------------------------------------------------
 
-def _pointers(ts: Sequence[Optional[torch.Tensor]], name: str, numels: Sequence[int], dtypes, optional: bool = False):
+def _pointers(ts: Sequence[Optional[torch.Tensor]], name: str, numels: Sequence[int], dtypes, optional: bool = False,
+              mixed: bool = False):
     """Device pointers of one kind of tensor, and their common dtype (None
-    where every tensor is None).  One pass with the checks of zs._dev, which is
+    where every tensor is None; of mixed ones the first's).  One pass with the checks of zs._dev, which is
     called only to say what is wrong: a list is some hundred tensors."""
     if len(ts) != len(numels):
         raise ValueError(f"{name}: {len(ts)} tensors, the list has {len(numels)}")
@@ -91,8 +101,9 @@ def _pointers(ts: Sequence[Optional[torch.Tensor]], name: str, numels: Sequence[
             zs._dev(t, f"{name}[{k}]")
         if kind is None:
             kind = t.dtype
-        if t.dtype != kind or kind not in dtypes:
-            raise TypeError(f"{name}[{k}]: {t.dtype}; one of {', '.join(map(str, dtypes))}, the same for all")
+        if (t.dtype != kind and not mixed) or t.dtype not in dtypes:
+            raise TypeError(f"{name}[{k}]: {t.dtype}; one of {', '.join(map(str, dtypes))}"
+                            f"{'' if mixed else ', the same for all'}")
         if t.numel() != n:
             raise ValueError(f"{name}[{k}]: size mismatch")
         out.append(t.data_ptr())
@@ -156,6 +167,23 @@ class GradTensors(_List):
         pointers, dtype = _pointers(grads, "grads", self.numels, _FLOATS)
         self._set("ptr", grads, pointers)
         self.grad_dtype = zs.ZS_BF16 if dtype == torch.bfloat16 else zs.ZS_F32
+
+
+class MixedTensors(_List):
+    """Tensors in fp32 and bf16, each its own, for grad_norms_sq_tensors and
+    grad_clip_tensors."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        tensors = list(tensors)
+        numels, device = _numels(tensors, "tensors")
+        super().__init__(MixedTensor, numels, device)
+        self.set(tensors)
+
+    def set(self, tensors: Sequence[torch.Tensor]) -> None:
+        """Other tensors of the same sizes (in either dtype)."""
+        pointers, _ = _pointers(tensors, "tensors", self.numels, _FLOATS, mixed=True)
+        self._set("ptr", tensors, pointers)
+        self.array["dtype"][:self.count] = [zs.ZS_BF16 if t.dtype == torch.bfloat16 else zs.ZS_F32 for t in tensors]
 
 
 class _StepList(_List):
@@ -375,3 +403,54 @@ def adamw_step_tensors_q8_dev(scalars_dev: torch.Tensor, tensors: AdamWQ8Tensors
         _scalars_dev(scalars_dev, AdamWQ8Scalars, "adamw_step_tensors_q8_dev"), tensors.address, tensors.count,
         tensors.param_dtype, tensors.grad_dtype, zs._norm(norm_sq, "adamw_step_tensors_q8_dev"),
         zs._stream(stream)))
+
+
+def _mixed_list(ts) -> MixedTensors:
+    return ts if isinstance(ts, MixedTensors) else MixedTensors(list(ts))
+
+
+def grad_norms_sq_tensors_workspace_bytes(grads: Union[MixedTensors, Sequence[torch.Tensor]]) -> int:
+    grads = _mixed_list(grads)
+    return int(_lib().grad_norms_sq_tensors_workspace_bytes(grads.address, grads.count))
+
+
+def grad_norms_sq_tensors(grads: Union[MixedTensors, Sequence[torch.Tensor]], grad_scale: float, out: torch.Tensor,
+                          norms: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """out[0] (fp64, device) = the squared norm of a list in fp32 and bf16, and
+    norms[k] (fp64, device) that of each tensor: sums of (fl32(widen(grad) *
+    scale))^2 in binary64."""
+    grads = _mixed_list(grads)
+    grads.check("grad_norms_sq_tensors")
+    if out.dtype != torch.float64 or out.numel() < 1:
+        raise TypeError("grad_norms_sq_tensors: out must hold one float64")
+    if norms is not None and (norms.dtype != torch.float64 or norms.numel() < grads.count):
+        raise TypeError(f"grad_norms_sq_tensors: norms must hold {grads.count} float64")
+    if workspace is None:
+        # of the stream it is used on: freed at return, it is next used in that stream's order
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(max(grad_norms_sq_tensors_workspace_bytes(grads), 8), dtype=torch.uint8,
+                                    device=out.device)
+    zs._check("grad_norms_sq_tensors", _lib().grad_norms_sq_tensors(
+        grads.address, grads.count, float(grad_scale), zs._dev(norms, "norms") if norms is not None else None,
+        zs._dev(out, "out"), zs._dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        zs._stream(stream)))
+    return out
+
+
+def grad_clip_tensors(grads: Union[MixedTensors, Sequence[torch.Tensor]],
+                      out: Union[None, MixedTensors, Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
+                      max_norm: float = 0.0, norm_sq: Optional[torch.Tensor] = None, extra_norm_sq: float = 0.0,
+                      stream=None) -> None:
+    """out[k] = grads[k] * grad_scale * min(1, max_norm / (norm + 1e-6)), rounded to out[k]'s
+    dtype; out None: in place.  norm_sq (fp64, device): of the scaled gradients, as
+    grad_norms_sq_tensors forms it; a norm that is not finite changes nothing."""
+    grads = _mixed_list(grads)
+    out = grads if out is None else _mixed_list(out)
+    grads.check("grad_clip_tensors")
+    out.check("grad_clip_tensors")
+    if out.numels != grads.numels:
+        raise ValueError("grad_clip_tensors: out has one tensor per gradient, of its size")
+    zs._check("grad_clip_tensors", _lib().grad_clip_tensors(
+        grads.address, out.address, grads.count, float(grad_scale), float(max_norm), float(extra_norm_sq),
+        zs._norm(norm_sq, "grad_clip_tensors"), zs._stream(stream)))

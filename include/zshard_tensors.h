@@ -53,6 +53,47 @@ ZS_API int64_t grad_norm_sq_tensors_workspace_bytes(const zs_tensor* grads, int3
 ZS_API int32_t grad_norm_sq_tensors(const zs_tensor* grads, int32_t count, int32_t grad_dtype, double grad_scale,
                                     double* out_sq_dev, void* workspace, int64_t workspace_bytes, void* hip_stream);
 
+/* One tensor of a list of mixed precision. */
+typedef struct {
+    void* ptr;
+    int64_t numel;         /* at most 2^35 */
+    int32_t dtype;         /* ZS_F32 or ZS_BF16 */
+    int32_t reserved;      /* 0 */
+} zs_mixed_tensor;
+
+/*
+ * grad_norms_sq_tensors — the squared norms of a list of gradients in fp32 and
+ * bf16: of every tensor (norms_sq_dev[k]; NULL: not wanted) and of all
+ * (*out_sq_dev, the norm_sq_dev of the steps and of grad_clip_tensors).  As
+ * grad_norm_sq_tensors, with squares exact in binary64 and summed in binary64
+ * in a fixed order that depends only on the numels and dtypes; a tensor without
+ * elements has the norm 0, an empty list writes 0.
+ * grads: read; norms_sq_dev: `count` device doubles, written; out_sq_dev: device
+ * double, written; workspace: device, 8-byte aligned, at least
+ * grad_norms_sq_tensors_workspace_bytes bytes (host only; -1 for an invalid
+ * list), scratch owned by the caller until the stream has passed the call.
+ * Errors: ZS_EINVAL, ZS_EWORKSPACE, ZS_EOVERLAP (what is written with anything
+ * else of the call), ZS_EHIP.
+ */
+ZS_API int64_t grad_norms_sq_tensors_workspace_bytes(const zs_mixed_tensor* grads, int32_t count);
+ZS_API int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count, double grad_scale,
+                                     double* norms_sq_dev, double* out_sq_dev, void* workspace,
+                                     int64_t workspace_bytes, void* hip_stream);
+
+/*
+ * grad_clip_tensors — gradients scaled and clipped to a global norm, as tensors:
+ * out[k] = fl32(fl32(widen(grads[k]) * (float)grad_scale) * coef), rounded to out[k]'s
+ * dtype, with adamw_step's coef: 1 where norm_sq_dev is NULL or max_norm <= 0, else
+ * (float)min(1, max_norm / (sqrt(*norm_sq_dev + extra_norm_sq) + 1e-6)).  Where that sum is not
+ * finite nothing is written.  out[k] has grads[k]'s numel and either dtype; it may
+ * be grads[k] itself in the same dtype (in place), and shares no byte with
+ * another buffer of the call otherwise.
+ * Errors: ZS_EINVAL, ZS_EOVERLAP, ZS_EHIP.
+ */
+ZS_API int32_t grad_clip_tensors(const zs_mixed_tensor* grads, const zs_mixed_tensor* out, int32_t count,
+                                 double grad_scale, double max_norm, double extra_norm_sq, const double* norm_sq_dev,
+                                 void* hip_stream);
+
 /* One tensor of adamw_step_tensors. */
 typedef struct {
     void* param;           /* fp32 or bf16 (param_dtype), read-write */
