@@ -53,8 +53,10 @@ Over lists of matrices (include/zshard_matrices.h):
     orthogonalize_matrices(matrices, steps=5, coefficients=..., eps=1e-7, workspace=None)
     muon_step_matrices(hp, matrices, norm_sq=None, workspace=None)   _dev: muon_scalars_bytes(hp) in device memory
 
-TensorOptimizer(params, lr=..., state_bits=32 or 8) orders them, as
+TensorOptimizer(params, lr=..., state_bits=32 or 8) orders the calls over
+tensors and MuonOptimizer(matrices, lr=...) those over matrices, as
 ShardOptimizer does the calls over a flat shard.
+
 
 DeviceArena(nbytes, device) holds one physically contiguous block of device
 memory and hands out 2 MiB-aligned views of it (ShardOptimizer(arena=...)).
@@ -126,6 +128,7 @@ from .matrices import (  # noqa: F401
     product_add_matrices_workspace_bytes,
     update_scale,
 )
+from .muon_step import MuonOptimizer  # noqa: F401
 from .step import ShardOptimizer  # noqa: F401
 from .tensor_step import TensorOptimizer  # noqa: F401
 from .tensors import (  # noqa: F401

@@ -66,6 +66,31 @@ def _written(params: Sequence[torch.Tensor], copies) -> tuple:
     return lo, hi
 
 
+def _refuse_overlap(grads: zt.GradTensors, lo, hi) -> None:
+    """Refuse gradients that share memory with what a step writes (_written)."""
+    # the first buffer that is written and ends after a gradient's start, if any
+    at = np.searchsorted(hi, grads.array["ptr"][:grads.count], side="right")
+    lo = np.append(lo, np.uint64(0xFFFFFFFFFFFFFFFF))[at]
+    sizes = np.array(grads.numels) * (2 if grads.grad_dtype == zs.ZS_BF16 else 4)
+    if ((lo < grads.array["ptr"][:grads.count] + sizes.astype(np.uint64)) & (sizes > 0)).any():
+        raise ValueError("bind_grads: a gradient overlaps a parameter or a re-cast")
+
+
+def _decays(weight_decay: Union[float, Sequence[float]], count: int) -> list:
+    """One weight decay per tensor."""
+    decays = [float(weight_decay)] * count if np.isscalar(weight_decay) else [float(d) for d in weight_decay]
+    if len(decays) != count:
+        raise ValueError(f"weight_decay: {len(decays)} values for {count} tensors")
+    if not all(0.0 <= d < float("inf") for d in decays):
+        raise ValueError("weight_decay: finite values >= 0")
+    return decays
+
+
+def _given_norm(norm_sq: Optional[torch.Tensor], fn: str) -> Optional[torch.Tensor]:
+    zs._norm(norm_sq, fn)   # its checks
+    return norm_sq
+
+
 class TensorOptimizer:
     """AdamW over `params` (contiguous fp32 or bf16 GPU tensors of one dtype,
     updated in place).  param_bf16: for fp32 params, bf16 tensors (or None) that
@@ -84,11 +109,7 @@ class TensorOptimizer:
             raise ValueError("params: at least one tensor")
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        decays = [float(weight_decay)] * len(params) if np.isscalar(weight_decay) else [float(d) for d in weight_decay]
-        if len(decays) != len(params):
-            raise ValueError(f"weight_decay: {len(decays)} values for {len(params)} tensors")
-        if not all(0.0 <= d < float("inf") for d in decays):
-            raise ValueError("weight_decay: finite values >= 0")
+        decays = _decays(weight_decay, len(params))
         if param_bf16 is not None and len(param_bf16) != len(params):
             raise ValueError(f"param_bf16: {len(param_bf16)} tensors for {len(params)}")
         checked = zt.GradTensors(params)   # the tensors' checks, before anything is allocated
@@ -130,18 +151,13 @@ class TensorOptimizer:
         lst = zt.GradTensors(list(grads))
         if lst.numels != [p.numel() for p in self.params]:
             raise ValueError("bind_grads: one gradient per parameter, of its size")
-        # the first buffer that is written and ends after a gradient's start, if any
-        at = np.searchsorted(self._hi, lst.array["ptr"][:lst.count], side="right")
-        lo = np.append(self._lo, np.uint64(0xFFFFFFFFFFFFFFFF))[at]
-        sizes = np.array(lst.numels) * (2 if lst.grad_dtype == zs.ZS_BF16 else 4)
-        if ((lo < lst.array["ptr"][:lst.count] + sizes.astype(np.uint64)) & (sizes > 0)).any():
-            raise ValueError("bind_grads: a gradient overlaps a parameter or a re-cast")
+        _refuse_overlap(lst, self._lo, self._hi)
         for _, at, group in self._groups:
             group._take_grads(lst, at)
         self._grads = lst
 
-    def _check_clip(self) -> None:
-        if self.max_norm > 0 and not self.compute_norm:
+    def _check_clip(self, norm_sq: Optional[torch.Tensor] = None) -> None:
+        if self.max_norm > 0 and not self.compute_norm and norm_sq is None:
             raise ValueError("max_norm > 0 needs the norm: compute_norm")
 
     def _hp(self, decay: float, extra_norm_sq: float, t: int) -> zs.AdamWConfig:
@@ -151,17 +167,20 @@ class TensorOptimizer:
     def _group_seed(self, k: int) -> int:
         return (self.seed + k) % (1 << 32)
 
-    def step(self, grads: Optional[Sequence[torch.Tensor]] = None, extra_norm_sq: float = 0.0) -> None:
+    def step(self, grads: Optional[Sequence[torch.Tensor]] = None, extra_norm_sq: float = 0.0,
+             norm_sq: Optional[torch.Tensor] = None) -> None:
         """One step on `grads` (bound first, see bind_grads), or on the bound
-        ones.  extra_norm_sq: the other ranks' share of the squared norm.  The
+        ones.  norm_sq: the squared norm of the scaled gradients of more than
+        these tensors, formed already (fp64, device: one norm for a model that
+        two optimizers share); extra_norm_sq: the other ranks' share of it.  The
         step counter advances only once the update is enqueued."""
         if grads is not None:
             self.bind_grads(grads)
         if self._grads is None:
             raise RuntimeError("step() without gradients")
-        self._check_clip()
-        norm = None
-        if self.compute_norm:
+        self._check_clip(norm_sq)
+        norm = norm_sq
+        if norm is None and self.compute_norm:
             norm = zt.grad_norm_sq_tensors(self._grads, self.grad_scale, self.norm_sq, self._workspace)
         for k, (decay, _, lst) in enumerate(self._groups):
             hp = self._hp(decay, extra_norm_sq, self.t + 1)
@@ -171,11 +190,12 @@ class TensorOptimizer:
                 zt.adamw_step_tensors_q8(hp, lst, seed=self._group_seed(k), norm_sq=norm)
         self.t += 1
 
-    def capture(self, extra_norm_sq: float = 0.0) -> "CapturedTensorStep":
+    def capture(self, extra_norm_sq: float = 0.0, norm_sq: Optional[torch.Tensor] = None) -> "CapturedTensorStep":
         """Record one step on the bound gradients in a HIP graph that replays
-        every later step (its scalars are read from device memory).  Capturing
-        changes neither parameters nor moments."""
-        return CapturedTensorStep(self, extra_norm_sq)
+        every later step (its scalars are read from device memory; a norm_sq that
+        is given, from its tensor).  Capturing changes neither parameters nor
+        moments."""
+        return CapturedTensorStep(self, extra_norm_sq, norm_sq)
 
     def _moments(self, exp_avg, exp_avg_sq) -> zt.Q8Moments:
         return zt.Q8Moments(self._states, exp_avg, exp_avg_sq, [p.numel() for p in self.params])
@@ -218,11 +238,12 @@ class CapturedTensorStep:
     """One TensorOptimizer step captured in a HIP graph (TensorOptimizer.capture).
     replay() runs the next step, t + 1, on the gradients that were bound."""
 
-    def __init__(self, opt: TensorOptimizer, extra_norm_sq: float):
+    def __init__(self, opt: TensorOptimizer, extra_norm_sq: float, norm_sq: Optional[torch.Tensor] = None):
         if opt._grads is None:
             raise RuntimeError("capture() without bound gradients")
-        opt._check_clip()
+        opt._check_clip(norm_sq)
         self.opt, self.extra_norm_sq = opt, extra_norm_sq
+        self._norm = _given_norm(norm_sq, "capture")
         self._fixed = (opt.grad_scale, opt.compute_norm)   # in the recorded launches, not in device memory
         # what the graph reads and writes stays this object's, whatever is bound later
         self._grads = opt._grads
@@ -257,8 +278,8 @@ class CapturedTensorStep:
 
     def _body(self, warm_up_norm: Optional[torch.Tensor] = None) -> None:
         opt = self.opt
-        norm = None
-        if opt.compute_norm:
+        norm = self._norm
+        if norm is None and opt.compute_norm:
             norm = zt.grad_norm_sq_tensors(self._grads, opt.grad_scale, opt.norm_sq, opt._workspace)
         norm = norm if warm_up_norm is None else warm_up_norm
         self._dev.copy_(self._host, non_blocking=True)
@@ -273,7 +294,7 @@ class CapturedTensorStep:
         pinned scalars before rewriting them.  lr, betas, eps and max_norm are
         the optimizer's of now; grad_scale and compute_norm must be those of
         the capture (the norm was recorded with them)."""
-        self.opt._check_clip()
+        self.opt._check_clip(self._norm)
         if self._fixed != (self.opt.grad_scale, self.opt.compute_norm):
             raise RuntimeError("replay(): grad_scale or compute_norm changed since the capture")
         self._done.synchronize()
