@@ -39,13 +39,24 @@ struct Operand {
     int extent;        // rows (columns form: a multiple of 8)
 };
 
+// Device memory straight into LDS: 64 lanes x 16 bytes, lane after lane from
+// `lds` (of the whole wave) on.  In asm: of its own loads of this kind the compiler
+// does not know which LDS reads they meet, and puts a wait for all of them before
+// every transposing read (8192 x 8192 x 8192 with b's columns: 1097 -> 1272
+// TFLOP/s).  It does not wait for these at a barrier either: loads_done().
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(from)
+                 : "memory");   // M0 is not allocated: the compiler sets it before each use of its own
+}
+// Every load to LDS of this wave has arrived (of the others': a barrier after it).
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 template <int ROWS, int THREADS, bool COLS>
 struct Stager {
     static constexpr int kChunks = ROWS * kTileK / 8 / THREADS;
     static_assert(kChunks * 8 * THREADS == ROWS * kTileK, "whole rounds of 16-byte chunks");
     uint32_t off[kChunks];   // bytes from the operand's k position
-    const char* base;
-    int64_t step;            // bytes per k tile
+    uint64_t base, step;     // bytes; step per k tile
 
     static __device__ __forceinline__ int swizzle(int k) {   // of a k row of the columns form, in chunks
         if constexpr (ROWS >= 128) return 2 * ((k & 3) | ((k >> 3) & 1) << 2);
@@ -66,20 +77,17 @@ struct Stager {
                 off[i] = (uint32_t)(((int64_t)at * o.pitch + c * 8) * 2);
             }
         }
-        if constexpr (COLS) {
-            base = reinterpret_cast<const char*>(o.p + first);
-            step = o.pitch * kTileK * 2;
-        } else {
-            base = reinterpret_cast<const char*>(o.p + (int64_t)first * o.pitch);
-            step = kTileK * 2;
-        }
+        base = reinterpret_cast<uint64_t>(o.p + (COLS ? (int64_t)first : (int64_t)first * o.pitch));
+        step = (uint64_t)(COLS ? o.pitch * kTileK * 2 : kTileK * 2);
     }
-    __device__ __forceinline__ void issue(Lds16* lds) {
+    // the next k tile to `lds` on; wave0: this wave's first thread
+    __device__ __forceinline__ void issue(Lds16* lds, int wave0) {
+        const __amdgpu_buffer_rsrc_t from =
+            __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, 0xFFFFFFFFu, 0x00027000);
+        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)lds) + wave0 * 16;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(base + (int64_t)off[i]),
-                (__attribute__((address_space(3))) void*)(lds + (i * THREADS + (threadIdx.x & ~63u)) * 8), 16, 0, 0);
+            load_to_lds(from, off[i], (uint32_t)__builtin_amdgcn_readfirstlane((int)(at + i * THREADS * 16)));
         base += step;
     }
     // the fragment of 16 rows from `row` and k from 32 * ks: lane l holds row l % 16, k = 8 (l / 16) ...
@@ -106,6 +114,16 @@ struct Stager {
 };
 
 // acc[i][j]: rows m = wave row + 16 i + lane % 16, columns n = wave column + 16 j + 4 (lane / 16) + 0..3
+//
+// Two k tiles are in LDS: one is multiplied while the next one's loads arrive.
+// A tile is worked through in phases of two rows of fragments; each phase first
+// starts the LDS reads of the next one's fragments, so that they arrive behind
+// its matrix instructions.  The last phase's are in the next tile: before it
+// comes the barrier, and after the barrier the loads of the tile after that,
+// which have a whole tile's time.  8192 x 8192 x 8192 in fp16, against reading
+// each phase's fragments at its start: 1235 -> 1295 TFLOP/s with b's rows, 1033
+// -> 1272 with its columns (a library product: 1315, 1249; on zeros, which
+// do not reach the power limit, 1561 and 1575).
 template <class T, bool BF16, bool BCOLS>
 __device__ __forceinline__ void multiply(const Operand& a, const Operand& b, int m0, int n0, int tiles, Lds16* lds,
                                          f32x4 (&acc)[T::MI][T::NI]) {
@@ -113,38 +131,65 @@ __device__ __forceinline__ void multiply(const Operand& a, const Operand& b, int
     Stager<T::BN, T::kThreads, BCOLS> sb;
     sa.init(a, m0);
     sb.init(b, n0);
-    const int wave = threadIdx.x >> 6, wm = (wave / T::WN) * (T::BM / T::WM), wn = (wave % T::WN) * (T::BN / T::WN);
+    const int wave0 = __builtin_amdgcn_readfirstlane((int)(threadIdx.x & ~63u)), wave = wave0 >> 6;
+    const int wm = (wave / T::WN) * (T::BM / T::WM), wn = (wave % T::WN) * (T::BN / T::WN);
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int j = 0; j < T::NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     if (tiles == 0) return;
-    sa.issue(lds);
-    sb.issue(lds + T::BM * kTileK);
-    __syncthreads();
+    constexpr int kG = T::MI / 2, kPhases = 2 * kG;   // phases of 32 of a tile's 64 k; of all
+    constexpr int kB = T::BM * kTileK, kPer = (T::NI + kG - 1) / kG;
     Lds16 *cur = lds, *next = lds + T::kStage;
+    sa.issue(cur, wave0);
+    sb.issue(cur + kB, wave0);
+    loads_done();
+    __syncthreads();
+    if (tiles > 1) {
+        sa.issue(next, wave0);
+        sb.issue(next + kB, wave0);
+    }
+    i16x8 fa[2][2], fb[2][T::NI];
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j) fb[0][j] = sb.fragment(cur + kB, wn + 16 * j, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) fa[0][i] = sa.fragment(cur, wm + 16 * i, 0);
     for (int t = 0; t < tiles; ++t) {
-        if (t + 1 < tiles) {
-            sa.issue(next);
-            sb.issue(next + T::BM * kTileK);
+#pragma unroll
+        for (int q = 0; q < kPhases; ++q) {
+            const int ks = q / kG, g = q % kG;
+            if (q == kPhases - 1) {
+                loads_done();
+                __syncthreads();
+                if (t + 2 < tiles) {
+                    sa.issue(cur, wave0);
+                    sb.issue(cur + kB, wave0);
+                }
+                // (past the last tile: what the other buffer held, not used)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fa[(q + 1) & 1][i] = sa.fragment(next, wm + 16 * i, 0);
+#pragma unroll
+                for (int j = 0; j < T::NI; ++j) fb[0][j] = sb.fragment(next + kB, wn + 16 * j, 0);
+            } else {
+                const int s = (q + 1) / kG, h = (q + 1) % kG;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fa[(q + 1) & 1][i] = sa.fragment(cur, wm + 32 * h + 16 * i, s);
+                if (ks == 0) {
+#pragma unroll
+                    for (int j = g * kPer; j < (g + 1) * kPer && j < T::NI; ++j) fb[1][j] = sb.fragment(cur + kB, wn + 16 * j, 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < T::NI; ++j) acc[2 * g + i][j] = mfma<BF16>(fb[ks][j], fa[q & 1][i], acc[2 * g + i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int ks = 0; ks < kTileK / 32; ++ks) {
-            i16x8 fa[T::MI], fb[T::NI];
-#pragma unroll
-            for (int j = 0; j < T::NI; ++j) fb[j] = sb.fragment(cur + T::BM * kTileK, wn + 16 * j, ks);
-#pragma unroll
-            for (int i = 0; i < T::MI; ++i) fa[i] = sa.fragment(cur, wm + 16 * i, ks);
-#pragma unroll
-            for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-                for (int j = 0; j < T::NI; ++j) acc[i][j] = mfma<BF16>(fb[j], fa[i], acc[i][j]);
-        }
-        __syncthreads();
         Lds16* const x = cur;
         cur = next;
         next = x;
     }
+    __syncthreads();   // the LDS is the caller's again
 }
 
 }  // namespace zs
