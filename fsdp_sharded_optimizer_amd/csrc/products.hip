@@ -38,15 +38,40 @@ __device__ __forceinline__ void tile_in_triangle(uint32_t t, uint32_t& i, uint32
     j = t - r * (r + 1) / 2;
 }
 
-// Calls f(row, column, four consecutive columns' values) for a wave's part of a tile.
-template <class T, class F>
-__device__ __forceinline__ void for_each4(const f32x4 (&acc)[T::MI][T::NI], int m0, int n0, F&& f) {
-    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int row = m0 + (wave / T::WN) * (T::BM / T::WM) + (l & 15), col = n0 + (wave % T::WN) * (T::BN / T::WN) + (l >> 4) * 4;
+// Calls f(row, column, x) for every eight neighbouring columns' values x[8] that this
+// lane has of a tile.
+template <class T, bool BCOLS, class F>
+__device__ __forceinline__ void each_row(const f32x4 (&acc)[T::MI][T::NI], int m0, int n0, F&& f) {
+    int row, column;
+    lane_place<T>(m0, n0, row, column);
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j) f(row + 16 * i, col + 16 * j, acc[i][j]);
+        for (int u = 0; u < T::NI / 2; ++u) {
+            f32x4 p[2];
+            pair_of<T, BCOLS>(acc, i, u, p);
+            float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
+            f(row + i, column + 32 * u, x);
+        }
+}
+// Calls f(row, column, x) for every MI neighbouring rows' values x[MI] of one column.
+template <class T, bool BCOLS, class F>
+__device__ __forceinline__ void each_column(const f32x4 (&acc)[T::MI][T::NI], int m0, int n0, F&& f) {
+    int row, column;
+    lane_place<T>(m0, n0, row, column);
+#pragma unroll
+    for (int u = 0; u < T::NI / 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            float x[T::MI];
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i) {
+                f32x4 p[2];
+                pair_of<T, BCOLS>(acc, i, u, p);
+                x[i] = p[h / 4][h % 4];
+            }
+            f(row, column + 32 * u + h, x);
+        }
 }
 
 template <class T>
@@ -57,40 +82,110 @@ __device__ __forceinline__ Lds16* tile_lds() {
 
 // --- the caller's products ---------------------------------------------------
 
-// four values, or those before the row's end, at any element alignment
-__device__ __forceinline__ f32x4 load4(const void* p, int bf16, int64_t at, int left) {
-    float x[4] = {0, 0, 0, 0};
-    if (bf16) {
-        const uint16_t* const q = static_cast<const uint16_t*>(p) + at;
-        if (left >= 4) return ld4<true>(q);
-        for (int j = 0; j < left; ++j) x[j] = bf16_to_f32(q[j]);
-    } else {
-        const float* const q = static_cast<const float*>(p) + at;
-        if (left >= 4) return ld4<true>(q);
-        for (int j = 0; j < left; ++j) x[j] = q[j];
-    }
-    return f32x4{x[0], x[1], x[2], x[3]};
-}
-__device__ __forceinline__ void store4(float* p, const f32x4& x, int left) {
-    if (left >= 4) {
-        *reinterpret_cast<f32x4_any*>(p) = x;
+// N neighbouring values at any element alignment, or those before the row's end.
+template <int N>
+__device__ __forceinline__ void load_run(const float* p, int left, float (&x)[N]) {
+    if (N % 4 == 0 && left >= N) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            const f32x4 v = reinterpret_cast<const f32x4_any*>(p)[k];
+            x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+        }
         return;
     }
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    for (int j = 0; j < left; ++j) p[j] = v[j];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = j < left ? p[j] : 0.0f;
 }
-__device__ __forceinline__ void store4(uint16_t* p, const f32x4& x, int left) {
-    const uint32_t a = pack_bf16x2(x.x, x.y), b = pack_bf16x2(x.z, x.w);
-    if (left >= 4) {
-        *reinterpret_cast<u32x2_any*>(p) = u32x2{a, b};
+template <int N>
+__device__ __forceinline__ void load_run(const uint16_t* p, int left, float (&x)[N]) {
+    if (N == 8 && left >= N) {
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(p);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = bf16_to_f32(w[j / 2] >> (16 * (j % 2)) & 0xFFFFu);
         return;
     }
-    const uint32_t v[4] = {a, a >> 16, b, b >> 16};
-    for (int j = 0; j < left; ++j) p[j] = (uint16_t)v[j];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = j < left ? bf16_to_f32(p[j]) : 0.0f;
+}
+template <int N>
+__device__ __forceinline__ void store_run(float* p, const float (&x)[N], int left) {
+    if (N % 4 == 0 && left >= N) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k)
+            reinterpret_cast<f32x4_any*>(p)[k] = f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < left) p[j] = x[j];
+}
+template <int N>
+__device__ __forceinline__ void store_run(uint16_t* p, const float (&x)[N], int left) {
+    if (N % 4 == 0 && left >= N) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) w[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+        if constexpr (N == 8) *reinterpret_cast<u32x4_any*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+        else if constexpr (N == 4) *reinterpret_cast<u32x2_any*>(p) = u32x2{w[0], w[1]};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < left) p[j] = (uint16_t)f32_to_bf16_rne(x[j]);
+}
+
+// The epilogue of a product: d from alpha times the sums and beta times c.
+template <class T, bool BCOLS, bool SYM, typename C, typename D>
+__device__ __forceinline__ void product_epilogue(f32x4 (&acc)[T::MI][T::NI], const C* c, D* d, int m, int n, int m0, int n0,
+                                                 float alpha, float beta) {
+    int row, column;
+    lane_place<T>(m0, n0, row, column);
+    const bool diagonal = SYM && m0 == n0;
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int u = 0; u < T::NI / 2; ++u) {
+            const int r = row + i, q = column + 32 * u, left = n - q;
+            if (r >= m || left <= 0) continue;
+            f32x4 p[2];
+            pair_of<T, BCOLS>(acc, i, u, p);
+            float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= alpha;
+            const int64_t at = (int64_t)r * n + q;
+            if (c != nullptr) {
+                float y[8];
+                load_run(c + at, left, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] += y[j] * beta;
+            }
+            if (!diagonal) store_run(d + at, x, left);
+            if constexpr (SYM) {   // (by rows: not exchanged)
+                acc[i][2 * u] = f32x4{x[0], x[1], x[2], x[3]};
+                acc[i][2 * u + 1] = f32x4{x[4], x[5], x[6], x[7]};
+            }
+        }
+    if constexpr (SYM) {
+        // The mirror; of a diagonal tile both triangles from the lower one (the three
+        // products of split values are not formed in the same order above it).
+        each_column<T, BCOLS>(acc, m0, n0, [&](int r, int q, const float (&x)[T::MI]) {
+            if (q >= n || r >= m) return;
+            if (!diagonal) {
+                store_run(d + (int64_t)q * n + r, x, m - r);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i) {
+                if (q > r + i || r + i >= m) continue;
+                st1(d + (int64_t)(r + i) * n + q, x[i]);
+                st1(d + (int64_t)q * n + r + i, x[i]);
+            }
+        });
+    }
 }
 
 template <class T, bool BCOLS, bool SYM>
-__global__ __launch_bounds__(T::kThreads) void products_kernel(const ProductBatch b) {
+__global__ __launch_bounds__(T::kThreads, 2) void products_kernel(const ProductBatch b) {
     uint32_t first;
     const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
     const ProductEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
@@ -104,49 +199,34 @@ __global__ __launch_bounds__(T::kThreads) void products_kernel(const ProductBatc
     const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN, m = (int)e.m, n = (int)e.n;
     f32x4 acc[T::MI][T::NI];
     multiply<T, true, BCOLS>(a, o, m0, n0, (int)e.k_tiles, tile_lds<T>(), acc);
-    const float alpha = b.alpha, beta = b.beta;
-    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 x) {
-        if (r >= m || q >= n) return;
-        const int64_t at = (int64_t)r * n + q;
-        const int left = n - q;
-        x *= alpha;
-        if (c != nullptr) x += load4(c, b.c_bf16, at, left) * beta;
-        if (!SYM || ti != tj) {
-            if (b.d_bf16) store4(static_cast<uint16_t*>(d) + at, x, left);
-            else store4(static_cast<float*>(d) + at, x, left);
-        }
-        if constexpr (SYM) {
-            // the mirror; of a diagonal tile both triangles from the lower one (the three
-            // products of split values are not formed in the same order above it)
-            const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= left || q + j > r) continue;
-                const int64_t mirror = (int64_t)(q + j) * n + r;
-                if (b.d_bf16) {
-                    const uint16_t y = (uint16_t)f32_to_bf16_rne(v[j]);
-                    if (ti == tj) static_cast<uint16_t*>(d)[at + j] = y;
-                    static_cast<uint16_t*>(d)[mirror] = y;
-                } else {
-                    if (ti == tj) static_cast<float*>(d)[at + j] = v[j];
-                    static_cast<float*>(d)[mirror] = v[j];
-                }
-            }
-        }
-    });
+    auto* const c16 = static_cast<const uint16_t*>(c);
+    auto* const c32 = static_cast<const float*>(c);
+    auto* const d16 = static_cast<uint16_t*>(d);
+    auto* const d32 = static_cast<float*>(d);
+    if constexpr (SYM) {   // c is of d's dtype
+        if (b.d_bf16) product_epilogue<T, BCOLS, SYM>(acc, c16, d16, m, n, m0, n0, b.alpha, b.beta);
+        else product_epilogue<T, BCOLS, SYM>(acc, c32, d32, m, n, m0, n0, b.alpha, b.beta);
+    } else if (b.c_bf16) {
+        if (b.d_bf16) product_epilogue<T, BCOLS, SYM>(acc, c16, d16, m, n, m0, n0, b.alpha, b.beta);
+        else product_epilogue<T, BCOLS, SYM>(acc, c16, d32, m, n, m0, n0, b.alpha, b.beta);
+    } else {
+        if (b.d_bf16) product_epilogue<T, BCOLS, SYM>(acc, c32, d16, m, n, m0, n0, b.alpha, b.beta);
+        else product_epilogue<T, BCOLS, SYM>(acc, c32, d32, m, n, m0, n0, b.alpha, b.beta);
+    }
 }
 
 // --- the Newton-Schulz steps ---------------------------------------------------
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ f32x4 widen4(const f16x4& x) { return f32x4{(float)x.x, (float)x.y, (float)x.z, (float)x.w}; }
-__device__ __forceinline__ f16x4 narrow4(const f32x4& x) {
-    return f16x4{(_Float16)x.x, (_Float16)x.y, (_Float16)x.z, (_Float16)x.w};
+// eight neighbouring fp16 values (16-byte aligned)
+__device__ __forceinline__ void load8(const _Float16* p, float (&x)[8]) {
+    const f16x8 v = *reinterpret_cast<const f16x8*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (float)v[j];
 }
 
 // S = X X^T, or b S + c S S: symmetric, tiles above the diagonal mirrored.
 template <class T, bool POLY>
-__global__ __launch_bounds__(T::kThreads) void ns_square_kernel(const NsBatch b) {
+__global__ __launch_bounds__(T::kThreads, 2) void ns_square_kernel(const NsBatch b) {
     uint32_t first, ti, tj;
     const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
     const NsEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
@@ -162,40 +242,78 @@ __global__ __launch_bounds__(T::kThreads) void ns_square_kernel(const NsBatch b)
     const float cb = b.sc_dev ? b.sc_dev->b : b.b, cc = (b.sc_dev ? b.sc_dev->c : b.c) * (1.0f / kNsScale);
     const _Float16* const s = reinterpret_cast<const _Float16*>(base + p.s());
     _Float16* const out = reinterpret_cast<_Float16*>(base + (POLY ? p.poly() : p.s()));
-    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 v) {
-        if (r >= mp || q >= mp) return;
-        const int64_t at = (int64_t)r * mp + q;
-        if constexpr (POLY) v = widen4(*reinterpret_cast<const f16x4*>(s + at)) * cb + v * cc;
-        else v *= 1.0f / kNsScale;
-        const f16x4 h = narrow4(v);
-        *reinterpret_cast<f16x4*>(out + at) = h;
-        if (ti != tj) {
+    int row, column;
+    lane_place<T>(m0, n0, row, column);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) out[(int64_t)(q + j) * mp + r] = h[j];
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int u = 0; u < T::NI / 2; ++u) {
+            const int64_t at = (int64_t)(row + i) * mp + column + 32 * u;
+            const bool inside = row + i < mp && column + 32 * u < mp;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = acc[i][2 * u + j / 4][j % 4];
+            if constexpr (POLY) {
+                float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (inside) load8(s + at, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = y[j] * cb + x[j] * cc;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= 1.0f / kNsScale;
+            }
+            f16x8 h;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = (_Float16)x[j];
+            if (inside) *reinterpret_cast<f16x8*>(out + at) = h;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][2 * u + j / 4][j % 4] = x[j];
         }
+    if (ti == tj) return;
+    each_column<T, false>(acc, m0, n0, [&](int r, int q, const float (&x)[T::MI]) {
+        if (r >= mp || q >= mp) return;   // both sides are whole runs of 8
+        typedef _Float16 Run __attribute__((ext_vector_type(T::MI)));
+        Run h;
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) h[i] = (_Float16)x[i];
+        *reinterpret_cast<Run*>(out + (int64_t)q * mp + r) = h;
     });
 }
 
-// a X + P X (P = b S + c S^2), X's pair as the residual
+// a X + P X (P = b S + c S^2), X's pair as the residual: f(row, column, x) for every
+// eight neighbouring columns, times kNsScale, inside the padded X
 template <class T, class F>
-__device__ __forceinline__ void ns_update(const char* base, const NsPlace& p, int which, float a, int m0, int n0, F&& f) {
+__device__ __forceinline__ void ns_update(const char* base, const NsPlace& p, int which, float a, int m0, int n0,
+                                          f32x4 (&acc)[T::MI][T::NI], F&& f) {
     const int mp = (int)p.mp, np = (int)p.np;
     const Operand poly = {reinterpret_cast<const uint16_t*>(base + p.poly()), mp, mp};
     const Operand x = {reinterpret_cast<const uint16_t*>(base + p.hi(which)), np, np};
-    f32x4 acc[T::MI][T::NI];
     multiply<T, false, true>(poly, x, m0, n0, mp / kTileK, tile_lds<T>(), acc);
     const _Float16* const hi = reinterpret_cast<const _Float16*>(base + p.hi(which));
     const _Float16* const lo = reinterpret_cast<const _Float16*>(base + p.lo(which));
-    for_each4<T>(acc, m0, n0, [&](int r, int q, f32x4 v) {
-        if (r >= mp || q >= np) return;
-        const int64_t at = (int64_t)r * np + q;
-        const f32x4 res = widen4(*reinterpret_cast<const f16x4*>(hi + at)) + widen4(*reinterpret_cast<const f16x4*>(lo + at)) * (1.0f / kNsLow);
-        f(r, q, at, res * a + v * (1.0f / kNsScale));
-    });
+    int row, column;
+    lane_place<T>(m0, n0, row, column);
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int u = 0; u < T::NI / 2; ++u) {
+            const int r = row + i, q = column + 32 * u;
+            if (r >= mp || q >= np) continue;
+            const int64_t at = (int64_t)r * np + q;
+            float h[8], l[8], y[8];
+            load8(hi + at, h);
+            load8(lo + at, l);
+            f32x4 v[2];
+            pair_of<T, true>(acc, i, u, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = (h[j] + l[j] * (1.0f / kNsLow)) * a + v[j / 4][j % 4] * (1.0f / kNsScale);
+            f(i, u, r, q, y);
+        }
 }
 
 template <class T>
-__global__ __launch_bounds__(T::kThreads) void ns_update_kernel(const NsBatch b) {
+__global__ __launch_bounds__(T::kThreads, 2) void ns_update_kernel(const NsBatch b) {
     uint32_t first, ti, tj;
     const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
     const NsEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
@@ -204,23 +322,24 @@ __global__ __launch_bounds__(T::kThreads) void ns_update_kernel(const NsBatch b)
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     _Float16* const hi = reinterpret_cast<_Float16*>(base + p.hi(1 - b.which));
     _Float16* const lo = reinterpret_cast<_Float16*>(base + p.lo(1 - b.which));
-    ns_update<T>(base, p, b.which, b.sc_dev ? b.sc_dev->a : b.a, (int)ti * T::BM, (int)tj * T::BN,
-                 [&](int, int, int64_t at, f32x4 v) {
-                     f16x4 h, l;
+    const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN;
+    f32x4 acc[T::MI][T::NI];
+    ns_update<T>(base, p, b.which, b.sc_dev ? b.sc_dev->a : b.a, m0, n0, acc, [&](int, int, int r, int q, const float (&x)[8]) {
+        const int64_t at = (int64_t)r * p.np + q;
+        f16x8 h, l;
 #pragma unroll
-                     for (int j = 0; j < 4; ++j) {
-                         _Float16 x, y;
-                         split_f16(v[j], x, y);
-                         h[j] = x;
-                         l[j] = y;
-                     }
-                     *reinterpret_cast<f16x4*>(hi + at) = h;
-                     *reinterpret_cast<f16x4*>(lo + at) = l;
-                 });
+        for (int j = 0; j < 8; ++j) {
+            _Float16 y, z;
+            split_f16(x[j], y, z);
+            h[j] = y;
+            l[j] = z;
+        }
+        *reinterpret_cast<f16x8*>(hi + at) = h;
+        *reinterpret_cast<f16x8*>(lo + at) = l;
+    });
 }
 
-// The epilogue of the last step: four values v of X's row r from column q on, still
-// times kNsScale, to their destination.
+// The epilogue of the last step: X, `scale` times what acc holds, to its destination.
 template <int KIND>
 struct Destination {
     using P = typename GradType<KIND != kFinalParamF32>::T;
@@ -232,26 +351,33 @@ struct Destination {
     __device__ __forceinline__ Destination(const FinalEntry& e, const MuonScalars& sc)
         : param(unpack_ptr<P>(e.lo[0], e.hi)), copy(unpack_ptr<uint16_t>(e.lo[1], e.hi >> 16)), m((int)e.m),
           n((int)(e.n & ~kTall)), tall((e.n & kTall) != 0), decay(sc.decay), step(sc.lr * e.scale) {}
-    __device__ __forceinline__ void put(int r, int q, f32x4 v) const {
-        if (r >= m || q >= n) return;
-        const int left = n - q;
-        if (!tall) {
-            const int64_t at = (int64_t)r * n + q;
-            if constexpr (KIND != kFinalBf16) v = load4(param, KIND == kFinalParamBf16, at, left) * decay - v * step;
-            store4(param + at, v, left);
-            if (KIND == kFinalParamF32 && copy != nullptr) store4(copy + at, v, left);
-            return;
-        }
-        const float x[4] = {v.x, v.y, v.z, v.w};
+    template <int N>
+    __device__ __forceinline__ void run(int64_t at, int left, float (&x)[N]) const {
+        if constexpr (KIND != kFinalBf16) {
+            float p[N];
+            load_run(param + at, left, p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j >= left) break;
-            const int64_t at = (int64_t)(q + j) * m + r;
-            float y = x[j];
-            if constexpr (KIND != kFinalBf16) y = widen(param[at]) * decay - y * step;
-            st1(param + at, y);
-            if (KIND == kFinalParamF32 && copy != nullptr) st1(copy + at, y);
+            for (int j = 0; j < N; ++j) x[j] = p[j] * decay - x[j] * step;
         }
+        store_run(param + at, x, left);
+        if (KIND == kFinalParamF32 && copy != nullptr) store_run(copy + at, x, left);
+    }
+    // by rows (not tall)
+    __device__ __forceinline__ void row(int r, int q, float (&x)[8], float scale) const {
+        if (r >= m || q >= n) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= scale;
+        run((int64_t)r * n + q, n - q, x);
+    }
+    // by columns (tall): a column of X is a row of the destination
+    template <class T, bool BCOLS>
+    __device__ __forceinline__ void columns(const f32x4 (&acc)[T::MI][T::NI], int m0, int n0, float scale) const {
+        each_column<T, BCOLS>(acc, m0, n0, [&](int r, int q, float (&x)[T::MI]) {
+            if (r >= m || q >= n) return;
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i) x[i] *= scale;
+            run((int64_t)q * m + r, m - r, x);
+        });
     }
 };
 
@@ -263,7 +389,7 @@ __device__ __forceinline__ bool skipped(const FinalBatch& b, const MuonScalars& 
 }
 
 template <class T, int KIND>
-__global__ __launch_bounds__(T::kThreads) void ns_final_kernel(const FinalBatch b) {
+__global__ __launch_bounds__(T::kThreads, 2) void ns_final_kernel(const FinalBatch b) {
     uint32_t first, ti, tj;
     const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
     const FinalEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
@@ -272,15 +398,26 @@ __global__ __launch_bounds__(T::kThreads) void ns_final_kernel(const FinalBatch 
     const Destination<KIND> to(e, sc);
     const NsPlace p(to.m, to.n);
     tile_in_bands(w - first, (uint32_t)((to.m + T::BM - 1) / T::BM), (uint32_t)((to.n + T::BN - 1) / T::BN), ti, tj);
-    ns_update<T>(b.ws + (int64_t)e.base * kNsUnit, p, b.which, sc.a, (int)ti * T::BM, (int)tj * T::BN,
-                 [&](int r, int q, int64_t, f32x4 v) { to.put(r, q, v * (1.0f / kNsScale)); });
+    const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN;
+    f32x4 acc[T::MI][T::NI];
+    const char* const base = b.ws + (int64_t)e.base * kNsUnit;
+    if (!to.tall) {
+        ns_update<T>(base, p, b.which, sc.a, m0, n0, acc,
+                     [&](int, int, int r, int q, float (&x)[8]) { to.row(r, q, x, 1.0f / kNsScale); });
+    } else {
+        ns_update<T>(base, p, b.which, sc.a, m0, n0, acc, [&](int i, int u, int, int, const float (&x)[8]) {
+            acc[i][2 * u] = f32x4{x[0], x[1], x[2], x[3]};
+            acc[i][2 * u + 1] = f32x4{x[4], x[5], x[6], x[7]};
+        });
+        to.template columns<T, false>(acc, m0, n0, 1.0f / kNsScale);
+    }
 }
 
 // --- matrices whose short side is at most 64 -------------------------------------
 
 // One partial sum of S from the pairs: hi hi^T + hi lo^T + lo hi^T (the fourth
 // product is below fp32's last bit).
-__global__ __launch_bounds__(T64::kThreads) void skinny_gram_kernel(const NsBatch b) {
+__global__ __launch_bounds__(T64::kThreads, 2) void skinny_gram_kernel(const NsBatch b) {
     uint32_t first;
     const NsEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
     const SkinnyPlace p(e.n);
@@ -302,7 +439,7 @@ __global__ __launch_bounds__(T64::kThreads) void skinny_gram_kernel(const NsBatc
     for (int i = 0; i < T64::MI; ++i)
 #pragma unroll
         for (int j = 0; j < T64::NI; ++j) acc[i][j] += sum[i][j];
-    for_each4<T64>(acc, 0, 0, [&](int r, int q, f32x4 v) { *reinterpret_cast<f32x4*>(out + r * kSkinny + q) = v; });
+    each_row<T64, false>(acc, 0, 0, [&](int r, int q, const float (&x)[8]) { store_run(out + r * kSkinny + q, x, 8); });
 }
 
 // 64 x 64 matrices in LDS, rows of 65 words.
@@ -335,7 +472,7 @@ __device__ __forceinline__ void square_product(const Square& x, const Square& y,
 // Q = M_1 M_2 ... with M = a I + b S + c S^2 and S <- M S M after each (all
 // polynomials of the first S: they commute), and Q as two fp16 values times a power
 // of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].
-__global__ __launch_bounds__(T64::kThreads) void skinny_steps_kernel(const NsBatch b) {
+__global__ __launch_bounds__(T64::kThreads, 2) void skinny_steps_kernel(const NsBatch b) {
     __shared__ Square s, t, m, q;
     const NsEntry e = b.e[blockIdx.x];
     const SkinnyPlace p(e.n);
@@ -402,7 +539,7 @@ __global__ __launch_bounds__(T64::kThreads) void skinny_steps_kernel(const NsBat
 }
 
 template <int KIND>
-__global__ __launch_bounds__(T64::kThreads) void skinny_final_kernel(const FinalBatch b) {
+__global__ __launch_bounds__(T64::kThreads, 2) void skinny_final_kernel(const FinalBatch b) {
     uint32_t first;
     const FinalEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
     const MuonScalars& sc = b.sc_dev ? *b.sc_dev : b.sc;
@@ -416,7 +553,8 @@ __global__ __launch_bounds__(T64::kThreads) void skinny_final_kernel(const Final
     f32x4 acc[T64::MI][T64::NI];
     multiply<T64, false, true>(q, x, 0, n0, 3, tile_lds<T64>(), acc);
     const float scale = *reinterpret_cast<const float*>(base + p.scale());
-    for_each4<T64>(acc, 0, n0, [&](int r, int c, f32x4 v) { to.put(r, c, v * scale); });
+    if (to.tall) to.template columns<T64, true>(acc, 0, n0, scale);
+    else each_row<T64, true>(acc, 0, n0, [&](int r, int c, float (&x)[8]) { to.row(r, c, x, scale); });
 }
 
 template <class T>
