@@ -233,7 +233,7 @@ Matrix matrix_of(const zs_orthogonal& x) { return Matrix{x.in, nullptr, x.out, n
 
 // A list is worked through in groups of consecutive matrices that share the
 // workspace: as many as kGroupElems elements hold, one at least.
-constexpr int64_t kGroupElems = int64_t(1) << 27;
+constexpr int64_t kGroupElems = int64_t(1) << 29;
 struct Group {
     int32_t first, last;      // [first, last)
     int64_t units;            // of kNsUnit
