@@ -7,7 +7,9 @@
 namespace zs {
 
 // Matrices in the workspace have both sides padded to whole k tiles with zeros,
-// so the products need no tails.
+// so the products need no tails.  Those of the Newton-Schulz steps lie in blocks of
+// 64 x 64 (mfma_tile.h): what a tile reads and writes is a few pieces of 8 KiB
+// instead of hundreds of rows some pages apart.
 constexpr int64_t kPadSide = 64;
 __host__ __device__ __forceinline__ int64_t pad_side(int64_t n) { return (n + kPadSide - 1) / kPadSide * kPadSide; }
 
@@ -72,7 +74,7 @@ constexpr float kNsLow = 2048.0f;
 __device__ __forceinline__ void split_f16(float x, _Float16& hi, _Float16& lo) {
     asm("" : "+v"(x));
     hi = (_Float16)x;
-    lo = (_Float16)((x - (float)hi) * kNsLow);
+    lo = (_Float16)__builtin_fmaf((float)hi, -kNsLow, x * kNsLow);
 }
 struct NsEntry {
     uint32_t base;         // in kNsUnit

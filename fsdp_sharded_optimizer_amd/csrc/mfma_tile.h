@@ -48,12 +48,33 @@ __device__ __forceinline__ int column_of(int p) {    // p: 16 j + 4 g + s
 }
 
 // An operand's place in device memory, k innermost ("rows": X[row][k]) or
-// outermost ("columns": X[k][row]).
+// outermost ("columns": X[k][row]).  Its rows (columns) come in blocks of 64, which
+// a row-major matrix has 64 rows (64 elements) apart; a matrix in the workspace
+// is kept in blocks of 64 x 64, each 8 KiB in one piece (blocked()).
 struct Operand {
     const uint16_t* p;
-    int64_t pitch;     // elements
+    int64_t pitch;     // elements from one row (k row) to the next
+    int64_t block;     // from one block of rows (columns) to the next
+    int64_t step;      // from one k tile to the next
     int extent;        // rows (columns form: a multiple of 8)
 };
+__device__ __forceinline__ Operand by_rows(const uint16_t* p, int64_t pitch, int extent) {
+    return Operand{p, pitch, 64 * pitch, kTileK, extent};
+}
+__device__ __forceinline__ Operand by_columns(const uint16_t* p, int64_t pitch, int extent) {
+    return Operand{p, pitch, 64, kTileK * pitch, extent};
+}
+constexpr int kBlockElems = 64 * 64;
+// across: blocks in a row of them
+__device__ __forceinline__ Operand blocked_by_rows(const uint16_t* p, int across, int extent) {
+    return Operand{p, 64, (int64_t)across * kBlockElems, kBlockElems, extent};
+}
+__device__ __forceinline__ Operand blocked_by_columns(const uint16_t* p, int across, int extent) {
+    return Operand{p, 64, kBlockElems, (int64_t)across * kBlockElems, extent};
+}
+__host__ __device__ __forceinline__ int64_t blocked(int row, int column, int across) {
+    return ((int64_t)(row >> 6) * across + (column >> 6)) * kBlockElems + (row & 63) * 64 + (column & 63);
+}
 
 // Device memory straight into LDS: 64 lanes x 16 bytes, lane after lane from
 // `lds` (of the whole wave) on.  In asm: of its own loads of this kind the compiler
@@ -92,16 +113,16 @@ struct Stager {
                 constexpr int per = ROWS / 8;
                 const int k = p / per, c = (p % per) ^ swizzle(k);
                 const int at = min(first + c * 8, o.extent - 8) - first;   // past the edge: some column, not used
-                off[i] = (uint32_t)(((int64_t)k * o.pitch + at) * 2);
+                off[i] = (uint32_t)((k * o.pitch + (at >> 6) * o.block + (at & 63)) * 2);
             } else {
                 const int row = p / 8, c = (p % 8) ^ swizzle(row);
                 const int of = SIDE == kA ? row_of<T>(row) : column_of<T>(row);
                 const int at = min(first + of, o.extent - 1) - first;
-                off[i] = (uint32_t)(((int64_t)at * o.pitch + c * 8) * 2);
+                off[i] = (uint32_t)(((at >> 6) * o.block + (at & 63) * o.pitch + c * 8) * 2);
             }
         }
-        base = reinterpret_cast<uint64_t>(o.p + (SIDE == kBCols ? (int64_t)first : (int64_t)first * o.pitch));
-        step = (uint64_t)(SIDE == kBCols ? o.pitch * kTileK * 2 : kTileK * 2);
+        base = reinterpret_cast<uint64_t>(o.p + (first >> 6) * o.block);   // (tiles start on blocks)
+        step = (uint64_t)o.step * 2;
     }
     // the next k tile to `lds` on; wave0: this wave's first thread
     __device__ __forceinline__ void issue(Lds16* lds, int wave0) {
@@ -136,7 +157,7 @@ struct Stager {
     }
 };
 
-// acc: a tile's sums, to be read by rows_of_8 and columns_of_rows below.
+// acc: a tile's sums (pair_of and lane_place say where).
 //
 // Two k tiles are in LDS: one is multiplied while the next one's loads arrive.
 // A tile is worked through in phases of two rows of fragments; each phase first

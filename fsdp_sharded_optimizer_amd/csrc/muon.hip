@@ -190,9 +190,11 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const PackBatch b) {
                 h[j] = first_of;
                 l[j] = second_of;
             }
-            *reinterpret_cast<f16x8*>(hi + r * p.np + c) = h;
-            *reinterpret_cast<f16x8*>(lo + r * p.np + c) = l;
-            if (again != nullptr) *reinterpret_cast<f16x8*>(again + r * p.np + c) = h;
+            // (a tile is a block of the workspace)
+            const int64_t at = (int64_t)tile * (kSide * kSide) + (r % kSide) * kSide + c % kSide;
+            *reinterpret_cast<f16x8*>(hi + at) = h;
+            *reinterpret_cast<f16x8*>(lo + at) = l;
+            if (again != nullptr) *reinterpret_cast<f16x8*>(again + at) = h;
         });
 }
 

@@ -7,6 +7,7 @@
 namespace zs {
 namespace {
 
+constexpr int kRowsAtOnce = 4;
 using T256 = Tile<256, 256, 2, 4>;
 using T128 = Tile<128, 128, 2, 2>;
 using T64 = Tile<64, 64, 2, 2>;
@@ -22,12 +23,17 @@ __device__ __forceinline__ uint32_t tile_of(uint32_t w, uint32_t n) {
     return base + (uint32_t)xcd_slot(i, n - base);
 }
 
-// Tile t of a matrix of tm x tn tiles, as its row and column: bands of 4 rows.
+// Tile t of a matrix of tm x tn tiles, as its row and column: panels of 8 columns,
+// in them bands of 4 rows.  An XCD's 32 tiles share 4 rows and 8 columns of operands,
+// and the 8 XCDs' together 16 and 16 of a matrix of 16 rows: the wider operand
+// comes from memory once (against bands over all columns, 4096 x 88064 x 4096:
+// 1170 -> 1218 TFLOP/s).
 __device__ __forceinline__ void tile_in_bands(uint32_t t, uint32_t tm, uint32_t tn, uint32_t& i, uint32_t& j) {
-    constexpr uint32_t kBand = 4;
-    const uint32_t band = t / (kBand * tn), in = t - band * kBand * tn, h = min(kBand, tm - band * kBand);
-    i = band * kBand + in % h;
-    j = in / h;
+    constexpr uint32_t kPanel = 8, kBand = 4;
+    const uint32_t panel = t / (kPanel * tm), columns = min(kPanel, tn - panel * kPanel), in = t - panel * kPanel * tm;
+    const uint32_t band = in / (kBand * columns), rows = min(kBand, tm - band * kBand), at = in - band * kBand * columns;
+    i = band * kBand + at % rows;
+    j = panel * kPanel + at / rows;
 }
 // Tile t of a triangle: row i has i + 1 of them.
 __device__ __forceinline__ void tile_in_triangle(uint32_t t, uint32_t& i, uint32_t& j) {
@@ -192,8 +198,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void products_kernel(const ProductB
     uint32_t ti, tj;
     if constexpr (SYM) tile_in_triangle(w - first, ti, tj);
     else tile_in_bands(w - first, (e.m + T::BM - 1) / T::BM, (e.n + T::BN - 1) / T::BN, ti, tj);
-    const Operand a = {unpack_ptr<const uint16_t>(e.lo[0], e.hi[0]), (int64_t)e.lda, (int)e.m};
-    const Operand o = {unpack_ptr<const uint16_t>(e.lo[1], e.hi[0] >> 16), (int64_t)e.ldb, BCOLS ? (int)e.ldb : (int)e.n};
+    const Operand a = by_rows(unpack_ptr<const uint16_t>(e.lo[0], e.hi[0]), e.lda, (int)e.m);
+    const uint16_t* const right = unpack_ptr<const uint16_t>(e.lo[1], e.hi[0] >> 16);
+    const Operand o = BCOLS ? by_columns(right, e.ldb, (int)e.ldb) : by_rows(right, e.ldb, (int)e.n);
     const void* const c = unpack_ptr<const uint16_t>(e.lo[2], e.hi[1]);
     void* const d = unpack_ptr<uint16_t>(e.lo[3], e.hi[1] >> 16);
     const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN, m = (int)e.m, n = (int)e.n;
@@ -217,13 +224,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void products_kernel(const ProductB
 
 // --- the Newton-Schulz steps ---------------------------------------------------
 
-// eight neighbouring fp16 values (16-byte aligned)
-__device__ __forceinline__ void load8(const _Float16* p, float (&x)[8]) {
-    const f16x8 v = *reinterpret_cast<const f16x8*>(p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = (float)v[j];
-}
-
 // S = X X^T, or b S + c S S: symmetric, tiles above the diagonal mirrored.
 template <class T, bool POLY>
 __global__ __launch_bounds__(T::kThreads, 2) void ns_square_kernel(const NsBatch b) {
@@ -236,7 +236,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void ns_square_kernel(const NsBatch
     const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN, mp = (int)p.mp;
     const int k = POLY ? mp : (int)p.np;
     const uint16_t* const x = reinterpret_cast<const uint16_t*>(base + (POLY ? p.s() : p.hi(b.which)));
-    const Operand o = {x, k, mp};
+    const int across = mp / 64;
+    const Operand o = blocked_by_rows(x, k / 64, mp);
     f32x4 acc[T::MI][T::NI];
     multiply<T, false, false>(o, o, m0, n0, k / kTileK, tile_lds<T>(), acc);
     const float cb = b.sc_dev ? b.sc_dev->b : b.b, cc = (b.sc_dev ? b.sc_dev->c : b.c) * (1.0f / kNsScale);
@@ -248,26 +249,19 @@ __global__ __launch_bounds__(T::kThreads, 2) void ns_square_kernel(const NsBatch
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int u = 0; u < T::NI / 2; ++u) {
-            const int64_t at = (int64_t)(row + i) * mp + column + 32 * u;
             const bool inside = row + i < mp && column + 32 * u < mp;
-            float x[8];
+            const int64_t at = blocked(min(row + i, mp - 1), min(column + 32 * u, mp - 8), across);
+            f16x8 y, h;
+            if constexpr (POLY) y = *reinterpret_cast<const f16x8*>(s + at);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = acc[i][2 * u + j / 4][j % 4];
-            if constexpr (POLY) {
-                float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (inside) load8(s + at, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = y[j] * cb + x[j] * cc;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= 1.0f / kNsScale;
+            for (int j = 0; j < 8; ++j) {
+                float x = acc[i][2 * u + j / 4][j % 4];
+                if constexpr (POLY) x = __builtin_fmaf((float)y[j], cb, x * cc);
+                else x *= 1.0f / kNsScale;
+                acc[i][2 * u + j / 4][j % 4] = x;
+                h[j] = (_Float16)x;
             }
-            f16x8 h;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = (_Float16)x[j];
             if (inside) *reinterpret_cast<f16x8*>(out + at) = h;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][2 * u + j / 4][j % 4] = x[j];
         }
     if (ti == tj) return;
     each_column<T, false>(acc, m0, n0, [&](int r, int q, const float (&x)[T::MI]) {
@@ -276,40 +270,53 @@ __global__ __launch_bounds__(T::kThreads, 2) void ns_square_kernel(const NsBatch
         Run h;
 #pragma unroll
         for (int i = 0; i < T::MI; ++i) h[i] = (_Float16)x[i];
-        *reinterpret_cast<Run*>(out + (int64_t)q * mp + r) = h;
+        *reinterpret_cast<Run*>(out + blocked(q, r, across)) = h;
     });
 }
 
-// a X + P X (P = b S + c S^2), X's pair as the residual: f(row, column, x) for every
-// eight neighbouring columns, times kNsScale, inside the padded X
+// a X + P X (P = b S + c S^2), X's pair as the residual: f(i, u, row, column, x) for
+// every eight neighbouring columns inside the padded X, times kNsScale
 template <class T, class F>
 __device__ __forceinline__ void ns_update(const char* base, const NsPlace& p, int which, float a, int m0, int n0,
                                           f32x4 (&acc)[T::MI][T::NI], F&& f) {
-    const int mp = (int)p.mp, np = (int)p.np;
-    const Operand poly = {reinterpret_cast<const uint16_t*>(base + p.poly()), mp, mp};
-    const Operand x = {reinterpret_cast<const uint16_t*>(base + p.hi(which)), np, np};
+    const int mp = (int)p.mp, np = (int)p.np, across = np / 64;
+    const Operand poly = blocked_by_rows(reinterpret_cast<const uint16_t*>(base + p.poly()), mp / 64, mp);
+    const Operand x = blocked_by_columns(reinterpret_cast<const uint16_t*>(base + p.hi(which)), across, np);
     multiply<T, false, true>(poly, x, m0, n0, mp / kTileK, tile_lds<T>(), acc);
     const _Float16* const hi = reinterpret_cast<const _Float16*>(base + p.hi(which));
     const _Float16* const lo = reinterpret_cast<const _Float16*>(base + p.lo(which));
     int row, column;
     lane_place<T>(m0, n0, row, column);
+    // the loads of ROWS rows before the first use (both column groups of a row: they
+    // share its cache line)
+    constexpr int kRows = T::MI < kRowsAtOnce ? T::MI : kRowsAtOnce, kU = T::NI / 2;
 #pragma unroll
-    for (int i = 0; i < T::MI; ++i)
+    for (int i0 = 0; i0 < T::MI; i0 += kRows) {
+        f16x8 h[kRows][kU], l[kRows][kU];
 #pragma unroll
-        for (int u = 0; u < T::NI / 2; ++u) {
-            const int r = row + i, q = column + 32 * u;
-            if (r >= mp || q >= np) continue;
-            const int64_t at = (int64_t)r * np + q;
-            float h[8], l[8], y[8];
-            load8(hi + at, h);
-            load8(lo + at, l);
-            f32x4 v[2];
-            pair_of<T, true>(acc, i, u, v);
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[j] = (h[j] + l[j] * (1.0f / kNsLow)) * a + v[j / 4][j % 4] * (1.0f / kNsScale);
-            f(i, u, r, q, y);
-        }
+            for (int u = 0; u < kU; ++u) {
+                const int64_t at = blocked(min(row + i0 + i, mp - 1), min(column + 32 * u, np - 8), across);
+                h[i][u] = *reinterpret_cast<const f16x8*>(hi + at);
+                l[i][u] = *reinterpret_cast<const f16x8*>(lo + at);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                f32x4 v[2];
+                pair_of<T, true>(acc, i0 + i, u, v);
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = __builtin_fmaf((float)l[i][u][j], a * (1.0f / kNsLow),
+                                          __builtin_fmaf((float)h[i][u][j], a, v[j / 4][j % 4] * (1.0f / kNsScale)));
+                const int r = row + i0 + i, q = column + 32 * u;
+                if (r < mp && q < np) f(i0 + i, u, r, q, y);
+            }
+    }
 }
 
 template <class T>
@@ -325,7 +332,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void ns_update_kernel(const NsBatch
     const int m0 = (int)ti * T::BM, n0 = (int)tj * T::BN;
     f32x4 acc[T::MI][T::NI];
     ns_update<T>(base, p, b.which, b.sc_dev ? b.sc_dev->a : b.a, m0, n0, acc, [&](int, int, int r, int q, const float (&x)[8]) {
-        const int64_t at = (int64_t)r * p.np + q;
+        const int64_t at = blocked(r, q, (int)(p.np / 64));
         f16x8 h, l;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -424,8 +431,9 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_gram_kernel(const NsB
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const int64_t chunk = blockIdx.x - first, from = chunk * p.chunk, left = p.np / kTileK - from;
     const int tiles = (int)(left < p.chunk ? left : p.chunk);
-    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base) + from * kTileK;
-    const Operand hi = {x, p.np, (int)kSkinny}, lo = {x + p.x / 2, p.np, (int)kSkinny};
+    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base) + from * kBlockElems;
+    const int across = (int)(p.np / 64);
+    const Operand hi = blocked_by_rows(x, across, (int)kSkinny), lo = blocked_by_rows(x + p.x / 2, across, (int)kSkinny);
     f32x4 sum[T64::MI][T64::NI], acc[T64::MI][T64::NI];
     multiply<T64, false, false>(hi, lo, 0, 0, tiles, tile_lds<T64>(), sum);
     multiply<T64, false, false>(lo, hi, 0, 0, tiles, tile_lds<T64>(), acc);
@@ -548,8 +556,8 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_final_kernel(const Fi
     const SkinnyPlace p(to.n);
     const char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const int n0 = (int)(blockIdx.x - first) * T64::BN;
-    const Operand q = {reinterpret_cast<const uint16_t*>(base + p.q()), 3 * kSkinny, (int)kSkinny};
-    const Operand x = {reinterpret_cast<const uint16_t*>(base), p.np, (int)p.np};
+    const Operand q = by_rows(reinterpret_cast<const uint16_t*>(base + p.q()), 3 * kSkinny, (int)kSkinny);
+    const Operand x = blocked_by_columns(reinterpret_cast<const uint16_t*>(base), (int)(p.np / 64), (int)p.np);
     f32x4 acc[T64::MI][T64::NI];
     multiply<T64, false, true>(q, x, 0, n0, 3, tile_lds<T64>(), acc);
     const float scale = *reinterpret_cast<const float*>(base + p.scale());
