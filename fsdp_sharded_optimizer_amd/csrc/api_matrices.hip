@@ -21,18 +21,29 @@ bool sides_ok(int64_t rows, int64_t cols) {
            rows * cols <= kMaxElemsOfMatrix;
 }
 
-// The tile that a launch uses, from how many of each size it would have.
-// Smaller tiles read their operands more often from the caches, so the largest
-// one that still gives most of the 256 CUs a tile.
+// The tile that launches of a list use, from how many of each size one of them has
+// (a table of `most` matrices to a launch): the largest one of which there are
+// enough.  Larger tiles read their operands less often, so where a tile is long in k
+// 192 of them (on 256 CUs) are enough; short ones are mostly their first loads and their
+// epilogue, of which smaller tiles have several to a CU at a time.  224 matrices of 251
+// x 683, k up to 683, 64 / 128 / 192 / 256 / 512 enough: gram 162 / 98 / 98 / 92 / 92 us, muon step 684 /
+// 685 / 684 / 684 / 632; 4096 x 4096 x 4096 (256 tiles of 256 x 256, 1024 of 128 x 128): 1221 and 1046 TFLOP/s.
 struct TileCount {
     int64_t of[3] = {0, 0, 0};
-    void add(int64_t rows, int64_t cols, bool triangle) {
+    int64_t matrices = 0, longest = 0;
+    void add(int64_t rows, int64_t cols, int64_t k, bool triangle) {
         for (int s = 0; s < 3; ++s) {
             const int64_t r = ceil_div(rows, tile_side(s));
             of[s] += triangle ? r * (r + 1) / 2 : r * ceil_div(cols, tile_side(s));
         }
+        ++matrices;
+        longest = std::max(longest, k);
     }
-    int size() const { return of[kTile256] >= 192 ? kTile256 : of[kTile128] >= 192 ? kTile128 : kTile64; }
+    int size(int64_t most) const {
+        const int64_t launches = ceil_div(std::max(matrices, (int64_t)1), most);
+        const int64_t enough = (longest >= 1024 ? 192 : 512) * launches;
+        return of[kTile256] >= enough ? kTile256 : of[kTile128] >= enough ? kTile128 : kTile64;
+    }
 };
 
 // Checks that every call shares: the list, and the workspace against `need`.
@@ -134,7 +145,7 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
         if (!p.gram) ranges.add(1, p.b, p.k * p.n * isz, false);
         if (!(p.c == p.d && c_dtype == d_dtype)) ranges.add(2, p.c, p.m * p.n * elem_size(c_dtype), false);
         ranges.add(3, p.d, p.m * p.n * elem_size(d_dtype), true);
-        tiles.add(p.m, p.n, p.gram);
+        tiles.add(p.m, p.n, p.k, p.gram);
     }
     if (count > 0) ranges.add(4, workspace, need, true);
     if (ranges.clash()) return ZS_EOVERLAP;
@@ -180,10 +191,10 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
     b.beta = (float)beta;
     b.c_bf16 = c_dtype == ZS_BF16;
     b.d_bf16 = d_dtype == ZS_BF16;
-    const int size = tiles.size();
+    const int size = tiles.size(sizeof(b.e) / sizeof(b.e[0]));
     constexpr bool kGram = std::is_same<T, zs_gram>::value;
     auto launch = [&](const ProductBatch& x, int64_t n) {
-        return launch_products(x, size, b_cols, kGram, n, as_stream(hip_stream));
+        return launch_products(x, size, b_cols, kGram, in_dtype != ZS_BF16, n, as_stream(hip_stream));
     };
     Filler<ProductBatch, decltype(launch)> fill(b, launch);
     int64_t at = 0;
@@ -201,7 +212,7 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
             if (!q.b.direct) o = ws + q.b_at, ldb = b_cols ? pad_side(p.n) : kp;
         }
         TileCount one;
-        one.add(p.m, p.n, kGram);
+        one.add(p.m, p.n, p.k, kGram);
         int e = 0;
         rc = fill.add(one.of[size], e);
         if (rc != ZS_OK) return rc;
@@ -403,11 +414,12 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
                 return ZS_OK;
             }
             ++others;
-            square.add(pad_side(x.m()), pad_side(x.m()), true);
-            wide.add(pad_side(x.m()), pad_side(x.n()), false);
+            square.add(pad_side(x.m()), pad_side(x.m()), x.m(), true);
+            wide.add(pad_side(x.m()), pad_side(x.n()), x.m(), false);
             return ZS_OK;
         });
-        const int square_size = square.size(), wide_size = wide.size();
+        constexpr int64_t kMost = sizeof(b.e) / sizeof(b.e[0]);
+        const int square_size = square.size(kMost), wide_size = wide.size(kMost);
         // one launch of the steps over the matrices of one kind; tiles(matrix): its workgroups
         auto phase = [&](bool of_skinny, auto tiles, auto launch) -> int32_t {
             Filler<NsBatch, decltype(launch)> fill(b, launch);
@@ -428,7 +440,7 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
                 rc = phase(false,
                            [&](const Matrix& x) {
                                TileCount one;
-                               one.add(pad_side(x.m()), pad_side(x.n()), kind_of != kNsUpdate);
+                               one.add(pad_side(x.m()), pad_side(x.n()), 0, kind_of != kNsUpdate);
                                return one.of[size];
                            },
                            [&](const NsBatch& x, int64_t tiles) { return launch_ns(x, kind_of, size, tiles, stream); });
@@ -459,7 +471,7 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
             rc = g.each(list, [&](const Matrix& x, int64_t unit) -> int32_t {
                 if ((x.m() <= kSkinny) != (of_skinny != 0)) return ZS_OK;
                 TileCount one;
-                one.add(x.m(), x.n(), false);
+                one.add(x.m(), x.n(), 0, false);
                 int e = 0;
                 const int32_t failed = fill.add(one.of[size], e);
                 if (failed != ZS_OK) return failed;

@@ -35,8 +35,10 @@ struct ProductBatch {
 };
 static_assert(sizeof(ProductBatch) <= 4096, "kernel arguments");
 // b_cols: b is k x n (else n x k).  sym: b is a's equal in value, m == n, and
-// tiles above the diagonal mirror those below.
-hipError_t launch_products(const ProductBatch& b, int size, bool b_cols, bool sym, int64_t tiles, hipStream_t stream);
+// tiles above the diagonal mirror those below.  split: k is three products of split
+// values.
+hipError_t launch_products(const ProductBatch& b, int size, bool b_cols, bool sym, bool split, int64_t tiles,
+                           hipStream_t stream);
 
 // Copies of operands into the kernels' form.
 enum StageKind : int { kStagePlain = 0, kStageHiHiLo = 1, kStageHiLoHi = 2 };

@@ -12,14 +12,14 @@ typedef short i16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileK = 64;
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr int kThreads = WM * WN * 64;
     static constexpr int TM = BM / WM, TN = BN / WN;      // a wave's part
     static constexpr int MI = TM / 16, NI = TN / 16;      // fragments of it
     static constexpr int kStage = (BM + BN) * kTileK;   // 16-bit elements
-    static constexpr unsigned kLds = 2 * kStage * 2;
+    static constexpr unsigned kLds = STAGES * kStage * 2;
 };
 
 template <bool BF16>
@@ -85,8 +85,10 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(from)
                  : "memory");   // M0 is not allocated: the compiler sets it before each use of its own
 }
-// Every load to LDS of this wave has arrived (of the others': a barrier after it).
-__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All loads to LDS of this wave but the last N have arrived (of the other waves': a
+// barrier after it).
+template <int N>
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 enum Side : int { kA, kB, kBCols };   // the left operand; the right one by rows; by columns
 
@@ -159,7 +161,9 @@ struct Stager {
 
 // acc: a tile's sums (pair_of and lane_place say where).
 //
-// Two k tiles are in LDS: one is multiplied while the next one's loads arrive.
+// One k tile in LDS is multiplied while the next STAGES - 1 ones' loads arrive.  Two
+// stages of the large tiles fill the LDS; a workgroup of small ones waits for little but
+// its loads, and has four.
 // A tile is worked through in phases of two rows of fragments; each phase first
 // starts the LDS reads of the next one's fragments, so that they arrive behind
 // its matrix instructions.  The last phase's are in the next tile: before it
@@ -185,15 +189,21 @@ __device__ __forceinline__ void multiply(const Operand& a, const Operand& b, int
     if (tiles == 0) return;
     constexpr int kG = T::MI / 2, kPhases = 2 * kG;   // phases of 32 of a tile's 64 k; of all
     constexpr int kAt = T::BM * kTileK, kPer = (T::NI + kG - 1) / kG;
-    Lds16 *cur = lds, *next = lds + T::kStage;
-    sa.issue(cur, wave0);
-    sb.issue(cur + kAt, wave0);
-    loads_done();
+    constexpr int kLoads = sa.kChunks + sb.kChunks;   // of one k tile, by a wave
+    constexpr int kMore = (T::STAGES - 2) * kLoads;   // that may be under way when the next tile is needed
+    auto stage = [&](int t) { return lds + t % T::STAGES * T::kStage; };
+    auto issue = [&](int t) {
+        Lds16* const to = stage(t);
+        sa.issue(to, wave0);
+        sb.issue(to + kAt, wave0);
+    };
+    issue(0);
+    loads_done<0>();
     __syncthreads();
-    if (tiles > 1) {
-        sa.issue(next, wave0);
-        sb.issue(next + kAt, wave0);
-    }
+#pragma unroll
+    for (int t = 1; t < T::STAGES; ++t)
+        if (t < tiles) issue(t);
+    Lds16 *cur = lds, *next = stage(1);
     i16x8 fa[2][2], fb[2][T::NI];
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) fb[0][j] = sb.fragment(cur + kAt, wn, j, 0);
@@ -204,12 +214,11 @@ __device__ __forceinline__ void multiply(const Operand& a, const Operand& b, int
         for (int q = 0; q < kPhases; ++q) {
             const int ks = q / kG, g = q % kG;
             if (q == kPhases - 1) {
-                loads_done();
+                // (with fewer tiles left than stages, fewer loads are under way)
+                if (kMore > 0 && t + T::STAGES <= tiles) loads_done<kMore>();
+                else loads_done<0>();
                 __syncthreads();
-                if (t + 2 < tiles) {
-                    sa.issue(cur, wave0);
-                    sb.issue(cur + kAt, wave0);
-                }
+                if (t + T::STAGES < tiles) issue(t + T::STAGES);
                 // (past the last tile: what the other buffer held, not used)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) fa[(q + 1) & 1][i] = sa.fragment(next, wm, i, 0);
@@ -230,9 +239,8 @@ __device__ __forceinline__ void multiply(const Operand& a, const Operand& b, int
                 for (int j = 0; j < T::NI; ++j) acc[2 * g + i][j] = mfma<BF16>(fb[ks][j], fa[q & 1][i], acc[2 * g + i][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        Lds16* const x = cur;
         cur = next;
-        next = x;
+        next = T::STAGES == 2 ? stage(t) : stage(t + 2);
     }
     __syncthreads();   // the LDS is the caller's again
 }

@@ -8,9 +8,9 @@ namespace zs {
 namespace {
 
 constexpr int kRowsAtOnce = 4;
-using T256 = Tile<256, 256, 2, 4>;
-using T128 = Tile<128, 128, 2, 2>;
-using T64 = Tile<64, 64, 2, 2>;
+using T256 = Tile<256, 256, 2, 4, 2>;
+using T128 = Tile<128, 128, 2, 2, 2>;
+using T64 = Tile<64, 64, 2, 2, 3>;
 
 // The tile that workgroup w of a launch runs.  gfx950 deals workgroups to its 8
 // XCDs in turn: runs of as many consecutive tiles as an XCD works on at a time
@@ -82,7 +82,7 @@ __device__ __forceinline__ void each_column(const f32x4 (&acc)[T::MI][T::NI], in
 
 template <class T>
 __device__ __forceinline__ Lds16* tile_lds() {
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * T::kStage];
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[T::STAGES * T::kStage];
     return (Lds16*)lds;
 }
 
@@ -141,12 +141,15 @@ __device__ __forceinline__ void store_run(uint16_t* p, const float (&x)[N], int 
 }
 
 // The epilogue of a product: d from alpha times the sums and beta times c.
-template <class T, bool BCOLS, bool SYM, typename C, typename D>
+enum Symmetry : int { kGeneral, kSymmetric, kSymmetricSplit };
+template <class T, bool BCOLS, int SYM, typename C, typename D>
 __device__ __forceinline__ void product_epilogue(f32x4 (&acc)[T::MI][T::NI], const C* c, D* d, int m, int n, int m0, int n0,
                                                  float alpha, float beta) {
     int row, column;
     lane_place<T>(m0, n0, row, column);
-    const bool diagonal = SYM && m0 == n0;
+    // of split values the three products are not formed in the same order above the
+    // diagonal: a diagonal tile's upper triangle is its lower one's mirror then
+    const bool diagonal = SYM != kGeneral && m0 == n0, mirrored = SYM == kSymmetricSplit && diagonal;
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
@@ -165,18 +168,17 @@ __device__ __forceinline__ void product_epilogue(f32x4 (&acc)[T::MI][T::NI], con
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] += y[j] * beta;
             }
-            if (!diagonal) store_run(d + at, x, left);
-            if constexpr (SYM) {   // (by rows: not exchanged)
+            if (!mirrored) store_run(d + at, x, left);
+            if constexpr (SYM != kGeneral) {   // (by rows: not exchanged)
                 acc[i][2 * u] = f32x4{x[0], x[1], x[2], x[3]};
                 acc[i][2 * u + 1] = f32x4{x[4], x[5], x[6], x[7]};
             }
         }
-    if constexpr (SYM) {
-        // The mirror; of a diagonal tile both triangles from the lower one (the three
-        // products of split values are not formed in the same order above it).
+    if constexpr (SYM != kGeneral) {
+        if (diagonal && !mirrored) return;
         each_column<T, BCOLS>(acc, m0, n0, [&](int r, int q, const float (&x)[T::MI]) {
             if (q >= n || r >= m) return;
-            if (!diagonal) {
+            if (!mirrored) {
                 store_run(d + (int64_t)q * n + r, x, m - r);
                 return;
             }
@@ -190,13 +192,13 @@ __device__ __forceinline__ void product_epilogue(f32x4 (&acc)[T::MI][T::NI], con
     }
 }
 
-template <class T, bool BCOLS, bool SYM>
+template <class T, bool BCOLS, int SYM>
 __global__ __launch_bounds__(T::kThreads, 2) void products_kernel(const ProductBatch b) {
     uint32_t first;
     const uint32_t w = tile_of<T>(blockIdx.x, gridDim.x);
     const ProductEntry e = b.e[find_tensor(b.tab, (uint32_t)__builtin_amdgcn_readfirstlane((int)w), first)];
     uint32_t ti, tj;
-    if constexpr (SYM) tile_in_triangle(w - first, ti, tj);
+    if constexpr (SYM != kGeneral) tile_in_triangle(w - first, ti, tj);
     else tile_in_bands(w - first, (e.m + T::BM - 1) / T::BM, (e.n + T::BN - 1) / T::BN, ti, tj);
     const Operand a = by_rows(unpack_ptr<const uint16_t>(e.lo[0], e.hi[0]), e.lda, (int)e.m);
     const uint16_t* const right = unpack_ptr<const uint16_t>(e.lo[1], e.hi[0] >> 16);
@@ -210,7 +212,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void products_kernel(const ProductB
     auto* const c32 = static_cast<const float*>(c);
     auto* const d16 = static_cast<uint16_t*>(d);
     auto* const d32 = static_cast<float*>(d);
-    if constexpr (SYM) {   // c is of d's dtype
+    if constexpr (SYM != kGeneral) {   // c is of d's dtype
         if (b.d_bf16) product_epilogue<T, BCOLS, SYM>(acc, c16, d16, m, n, m0, n0, b.alpha, b.beta);
         else product_epilogue<T, BCOLS, SYM>(acc, c32, d32, m, n, m0, n0, b.alpha, b.beta);
     } else if (b.c_bf16) {
@@ -566,11 +568,12 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_final_kernel(const Fi
 }
 
 template <class T>
-void launch_products_of(const ProductBatch& b, bool b_cols, bool sym, unsigned tiles, hipStream_t stream) {
+void launch_products_of(const ProductBatch& b, bool b_cols, bool sym, bool split, unsigned tiles, hipStream_t stream) {
     const dim3 grid(tiles), block(T::kThreads);
-    if (sym) hipLaunchKernelGGL((products_kernel<T, false, true>), grid, block, 0, stream, b);
-    else if (b_cols) hipLaunchKernelGGL((products_kernel<T, true, false>), grid, block, 0, stream, b);
-    else hipLaunchKernelGGL((products_kernel<T, false, false>), grid, block, 0, stream, b);
+    if (sym && split) hipLaunchKernelGGL((products_kernel<T, false, kSymmetricSplit>), grid, block, 0, stream, b);
+    else if (sym) hipLaunchKernelGGL((products_kernel<T, false, kSymmetric>), grid, block, 0, stream, b);
+    else if (b_cols) hipLaunchKernelGGL((products_kernel<T, true, kGeneral>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((products_kernel<T, false, kGeneral>), grid, block, 0, stream, b);
 }
 
 template <class T>
@@ -591,10 +594,11 @@ void launch_final_of(const FinalBatch& b, int kind, unsigned tiles, hipStream_t 
 
 }  // namespace
 
-hipError_t launch_products(const ProductBatch& b, int size, bool b_cols, bool sym, int64_t tiles, hipStream_t stream) {
-    if (size == kTile256) launch_products_of<T256>(b, b_cols, sym, (unsigned)tiles, stream);
-    else if (size == kTile128) launch_products_of<T128>(b, b_cols, sym, (unsigned)tiles, stream);
-    else launch_products_of<T64>(b, b_cols, sym, (unsigned)tiles, stream);
+hipError_t launch_products(const ProductBatch& b, int size, bool b_cols, bool sym, bool split, int64_t tiles,
+                           hipStream_t stream) {
+    if (size == kTile256) launch_products_of<T256>(b, b_cols, sym, split, (unsigned)tiles, stream);
+    else if (size == kTile128) launch_products_of<T128>(b, b_cols, sym, split, (unsigned)tiles, stream);
+    else launch_products_of<T64>(b, b_cols, sym, split, (unsigned)tiles, stream);
     return hipGetLastError();
 }
 

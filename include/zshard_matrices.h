@@ -68,7 +68,7 @@ ZS_API int32_t product_add_matrices(const zs_product* list, int32_t count, int32
 /* One product of gram_add_matrices. */
 typedef struct {
     const void* a;       /* rows x cols, of in_dtype, read */
-    const void* c;       /* a symmetric matrix of d's size (its lower triangle enters), of d_dtype, read; or NULL */
+    const void* c;       /* a symmetric matrix of d's size, of d_dtype, read; or NULL */
     void* d;             /* rows x rows (transposed: cols x cols), of d_dtype, written; may be c itself */
     int64_t rows, cols;
     int32_t transposed;  /* 0: a a^T; 1: a^T a */
@@ -79,8 +79,8 @@ typedef struct {
  * gram_add_matrices — d = alpha * a * a^T + beta * c (transposed: a^T * a) for every
  * entry of a list: the running statistics of matrix preconditioners.  As
  * product_add_matrices, but only the tiles on and below the diagonal are formed
- * and c's upper triangle does not enter: the upper triangle of d mirrors the
- * lower one.
+ * and the others mirror them: of c only the tiles on and below the diagonal are
+ * read, and d is symmetric, bit for bit, where c is.
  */
 ZS_API int64_t gram_add_matrices_workspace_bytes(const zs_gram* list, int32_t count, int32_t in_dtype);
 ZS_API int32_t gram_add_matrices(const zs_gram* list, int32_t count, int32_t in_dtype, int32_t d_dtype, double alpha,
