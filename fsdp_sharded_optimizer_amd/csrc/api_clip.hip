@@ -73,12 +73,14 @@ int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count, doubl
     TensorSums sums;
     std::memset(&sums, 0, sizeof(sums));
     int64_t entries = 0, tiles = 0, done = 0;   // of this launch; tensors of the launches before
+    const bool few = count > 0 && count <= kFewTensors && parts <= kFewPartials;   // (one launch)
     auto emit = [&]() -> int32_t {
         int32_t rc = fill.flush();
         if (rc != ZS_OK || sums.count == 0) return rc;
         sums.grid = (uint32_t)tiles;
         sums.partials = partials;
         sums.norms = norms + done;
+        if (few) return hip_status(launch_few_sums(sums, out_sq_dev, stream));
         rc = hip_status(launch_tensor_sums(sums, stream));
         partials += tiles;
         done += sums.count;
@@ -108,7 +110,7 @@ int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count, doubl
         sums.start[sums.count] = (uint32_t)tiles;
     }
     const int32_t rc = emit();
-    if (rc != ZS_OK) return rc;
+    if (rc != ZS_OK || few) return rc;
     return hip_status(launch_total(norms, count, out_sq_dev, stream));
 }
 

@@ -22,6 +22,11 @@ struct TensorSums {
 };
 static_assert(sizeof(TensorSums) <= 4096, "kernel arguments");
 hipError_t launch_tensor_sums(const TensorSums& b, hipStream_t stream);
+// A list of at most this many tensors and partials in one launch has its sums in one
+// more (1M gradients in 12 tensors: 21.0 -> 19.7 us with their clipping).
+constexpr int kFewTensors = 64;
+constexpr int64_t kFewPartials = 2048;
+hipError_t launch_few_sums(const TensorSums& b, double* out, hipStream_t stream);
 hipError_t launch_total(const double* norms, int64_t count, double* out, hipStream_t stream);
 
 constexpr int64_t kClipTile = 4096;

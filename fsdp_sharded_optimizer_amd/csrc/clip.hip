@@ -51,6 +51,28 @@ __global__ __launch_bounds__(kBlock) void total_kernel(const double* __restrict_
     if (threadIdx.x == 0) *out = s;
 }
 
+// Both in one workgroup, for a list of few tensors and partials: a wave adds the
+// partials of every 16th tensor, the first wave the tensors.
+constexpr int kFewThreads = 1024;
+__global__ __launch_bounds__(kFewThreads) void few_sums_kernel(const TensorSums b, double* __restrict__ out) {
+    __shared__ double norm[kFewTensors];
+    const uint32_t lane = threadIdx.x % 64;
+    for (uint32_t k = threadIdx.x / 64; k < b.count; k += kFewThreads / 64) {
+        const uint32_t to = b.start[k + 1];
+        double s = 0.0;
+        for (uint32_t i = b.start[k] + lane; i < to; i += 64) s += b.partials[xcd_slot(i, b.grid)];
+        s = wave_sum(s);
+        if (lane == 0) {
+            norm[k] = s;
+            b.norms[k] = s;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const double s = wave_sum(lane < b.count ? norm[lane] : 0.0);
+    if (lane == 0) *out = s;
+}
+
 template <typename S, typename D>
 __device__ __forceinline__ void clip_tile(const S* src, D* dst, int64_t n, int64_t tile, float scale, float coef) {
     constexpr int kQ = (int)(kClipTile / (kBlock * 4));
@@ -118,6 +140,11 @@ hipError_t launch_norms(const NormBatch& b, bool keep, int64_t tiles, float scal
 
 hipError_t launch_tensor_sums(const TensorSums& b, hipStream_t stream) {
     hipLaunchKernelGGL(tensor_sums_kernel, dim3(b.count), dim3(kBlock), 0, stream, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_few_sums(const TensorSums& b, double* out, hipStream_t stream) {
+    hipLaunchKernelGGL(few_sums_kernel, dim3(1), dim3(kFewThreads), 0, stream, b, out);
     return hipGetLastError();
 }
 

@@ -458,38 +458,36 @@ struct Square {
     float v[kSkinny * kPitch];
 };
 
-// f(row, column, value) of x y: wave w forms rows 16 w ... with the fp32 matrix
-// instruction (lane l: row l % 16 of a and column l % 16 of b at k = l / 16).
+// f(row, column, value) of x y: each of 16 waves forms 16 x 16 with the fp32 matrix
+// instruction (lane l: row l % 16 of a and column l % 16 of b at k = l / 16).  One
+// matrix's products follow one another, so that their latency counts: with 4 waves
+// of 16 x 64 each the kernel took 39 us (25 so).
+constexpr int kStepThreads = 1024;
 template <class F>
 __device__ __forceinline__ void square_product(const Square& x, const Square& y, F&& f) {
-    const int l = threadIdx.x & 63, row = (threadIdx.x >> 6) * 16, at = l & 15, kl = l >> 4;
-    f32x4 acc[4];
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, row = wave / 4 * 16, col = wave % 4 * 16, at = l & 15, kl = l >> 4;
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
-#pragma unroll 4
-    for (int k = 0; k < kSkinny; k += 4) {
-        const float a = x.v[(row + at) * kPitch + k + kl];
+    for (int k = 0; k < kSkinny; k += 8)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, y.v[(k + kl) * kPitch + 16 * j + at], acc[j], 0, 0, 0);
-    }
+        for (int h = 0; h < 2; ++h)
+            acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.v[(row + at) * kPitch + k + 4 * h + kl],
+                                                          y.v[(k + 4 * h + kl) * kPitch + col + at], acc[h], 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f(row + 4 * kl + i, 16 * j + at, acc[j][i]);
+    for (int i = 0; i < 4; ++i) f(row + 4 * kl + i, col + at, acc[0][i] + acc[1][i]);
 }
 
 // Q = M_1 M_2 ... with M = a I + b S + c S^2 and S <- M S M after each (all
 // polynomials of the first S: they commute), and Q as two fp16 values times a power
 // of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].
-__global__ __launch_bounds__(T64::kThreads, 2) void skinny_steps_kernel(const NsBatch b) {
+__global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatch b) {
     __shared__ Square s, t, m, q;
     const NsEntry e = b.e[blockIdx.x];
     const SkinnyPlace p(e.n);
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const float ca = b.sc_dev ? b.sc_dev->a : b.a, cb = b.sc_dev ? b.sc_dev->b : b.b, cc = b.sc_dev ? b.sc_dev->c : b.c;
     const float* const parts = reinterpret_cast<const float*>(base + p.parts());
-    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads) {
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += kStepThreads) {
         float x = 0.0f;
         for (int64_t k = 0; k < p.chunks; ++k) x += parts[k * (kSkinny * kSkinny) + i];
         s.v[i / kSkinny * kPitch + i % kSkinny] = x * (1.0f / (kNsScale * kNsScale));
@@ -503,17 +501,15 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_steps_kernel(const Ns
         });
         __syncthreads();
         const bool more = step + 1 < b.steps;
-        float kept[16];   // what a product of q or s by itself would overwrite
         if (step > 0) {
+            // q's own product: kept until every wave has read q
+            f32x4 kept;
             int n = 0;
             square_product(m, q, [&](int, int, float x) { kept[n++] = x; });
             __syncthreads();
-            n = 0;
-            const int l = threadIdx.x & 63, row = (threadIdx.x >> 6) * 16 + 4 * (l >> 4), col = l & 15;
+            const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) q.v[(row + i) * kPitch + 16 * j + col] = kept[n++];
+            for (int i = 0; i < 4; ++i) q.v[(wave / 4 * 16 + 4 * (l >> 4) + i) * kPitch + wave % 4 * 16 + (l & 15)] = kept[i];
         }
         if (more) {
             square_product(m, s, [&](int r, int c, float x) { t.v[r * kPitch + c] = x; });
@@ -524,19 +520,20 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_steps_kernel(const Ns
     }
     // the scale: Q's largest magnitude to [2^12, 2^13)
     float most = 0.0f;
-    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads)
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += kStepThreads)
         most = fmaxf(most, fabsf(q.v[i / kSkinny * kPitch + i % kSkinny]));
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
     __syncthreads();
     if ((threadIdx.x & 63) == 0) t.v[threadIdx.x >> 6] = most;
     __syncthreads();
-    most = fmaxf(fmaxf(t.v[0], t.v[1]), fmaxf(t.v[2], t.v[3]));
+#pragma unroll
+    for (int w = 0; w < kStepThreads / 64; ++w) most = fmaxf(most, t.v[w]);
     int exponent = 0;
     if (most > 0.0f && __builtin_isfinite(most)) (void)frexpf(most, &exponent);
     const float scale = ldexpf(1.0f, 13 - exponent);
     _Float16* const out = reinterpret_cast<_Float16*>(base + p.q());
-    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += T64::kThreads) {
+    for (int i = threadIdx.x; i < kSkinny * kSkinny; i += kStepThreads) {
         const int r = i / (int)kSkinny, c = i % (int)kSkinny;
         const float x = q.v[r * kPitch + c] * scale;
         _Float16 h, l;
@@ -615,7 +612,7 @@ hipError_t launch_skinny_gram(const NsBatch& b, int64_t tiles, hipStream_t strea
 }
 
 hipError_t launch_skinny_steps(const NsBatch& b, int64_t count, hipStream_t stream) {
-    hipLaunchKernelGGL(skinny_steps_kernel, dim3((unsigned)count), dim3(T64::kThreads), 0, stream, b);
+    hipLaunchKernelGGL(skinny_steps_kernel, dim3((unsigned)count), dim3(kStepThreads), 0, stream, b);
     return hipGetLastError();
 }
 
