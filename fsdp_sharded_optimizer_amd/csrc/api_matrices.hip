@@ -94,12 +94,13 @@ bool shape_ok(const zs_gram& p) {
 struct Placed {
     Side a, b;
     int64_t a_at, b_at, end;
+    bool shared;     // b is a's copy
 };
 Placed place(const Product& p, int32_t dtype, int64_t at) {
     Placed q;
     q.a = side_of(p.a, dtype, p.m, p.k, false, p.a_transposed);
     // a gram of bf16 values reads one copy twice
-    const bool one = p.gram && dtype == ZS_BF16;
+    const bool one = q.shared = p.gram && dtype == ZS_BF16;
     q.b = one ? q.a : side_of(p.b, dtype, p.n, p.k, !p.b_transposed, p.gram && p.a_transposed);
     q.a_at = at;
     at += ceil_div(q.a.bytes, 256) * 256;
@@ -170,7 +171,7 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
                 const Placed q = place(p, in_dtype, at);
                 at = q.end;
                 const Side& o = side == 0 ? q.a : q.b;
-                if (o.direct || (side == 1 && q.b_at == q.a_at)) continue;
+                if (o.direct || (side == 1 && q.shared)) continue;
                 const bool turned = p.gram || side == 0 ? p.a_transposed : false;
                 if (turned != (transposed != 0)) continue;
                 const int64_t rows = columns ? p.k : side == 0 ? p.m : p.n, cols = columns ? p.n : p.k;

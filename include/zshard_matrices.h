@@ -52,7 +52,8 @@ typedef struct {
  * binary32, one rounding to d_dtype.  fp32 inputs are split into two bf16
  * values each (16 significant bits) and three of their four products formed:
  * within 3 * 2^-16 of |a||b| per product (3e-6 of the result in the norm, as
- * measured); an input that is not finite makes what it enters NaN.  c is not read where it is NULL or beta is 0.  k = 0: d = beta * c.
+ * measured); an input that is not finite makes what it enters NaN.  c is not
+ * read where it is NULL or beta is 0.  k = 0: d = beta * c.
  * in_dtype, c_dtype, d_dtype: ZS_F32 or ZS_BF16; flags: ZS_TRANSPOSE_*.
  * No workspace is needed for bf16 inputs with every k a multiple of 64, no
  * ZS_TRANSPOSE_A, every n a multiple of 8 (or ZS_TRANSPOSE_B), and a and b on
@@ -100,15 +101,18 @@ typedef struct {
  * S = X X^T on the short side (a tall matrix: X <- a X + X (b S + c S^2), S = X^T X).
  * |in|_F is formed in binary64.  X is held scaled by 2^8 as a pair of fp16 values
  * (22 significant bits down to 2^-33, 2^-44 below: a matrix whose norm is 2^-20
- * eps or less), S and b S + c S^2 as one fp16 value each, so scaled;
- * the products take the pair's first value, sums are binary32, and a X the
- * whole pair.  What the linear term amplifies (small singular values, about a^steps
- * times) carries no fp16 rounding therefore: results are within 4e-3 of the
- * formula (relative, in the Frobenius norm; 3e-4 to 2e-3 as measured) for matrices
- * of any rank with the usual coefficients (3.4445, -4.775, 2.0315) and 5 steps, and their
- * rounding to bf16 (2^-8 of a value at most, 1.7e-3 in the norm) comes on top.  A zero matrix gives zeros, one
- * with a value that is not finite NaN.  steps: 1 to ZS_NS_MAX_STEPS; |a|, |b|, |c| at
- * most 32 and such that X stays bounded (fp16 ends at 255 times the scale); eps > 0.
+ * eps or less), S and b S + c S^2 as one fp16 value each, so scaled; the products
+ * take the pair's first value, sums are binary32, and a X the whole pair.  What the
+ * linear term amplifies (small singular values, about a^steps times) carries no
+ * fp16 rounding therefore: results are within 4e-3 of the formula (relative, in
+ * the Frobenius norm; 3e-4 to 2e-3 as measured) for matrices of any rank with the
+ * usual coefficients (3.4445, -4.775, 2.0315) and 5 steps, and their rounding to
+ * bf16 (2^-8 of a value at most, 1.7e-3 in the norm) comes on top.  Where the
+ * short side is 64 or less nothing is held in fp16 alone (the polynomials of S are
+ * formed in binary32 and applied to the pair): 1e-6 to 2e-4.
+ * A zero matrix gives zeros, one with a value that is not finite NaN.  steps: 1 to
+ * ZS_NS_MAX_STEPS; |a|, |b|, |c| at most 32 and such that X stays bounded (fp16 ends
+ * at 255 times the scale); eps: at least 1e-30.
  */
 #define ZS_NS_MAX_STEPS 32
 ZS_API int64_t orthogonalize_matrices_workspace_bytes(const zs_orthogonal* list, int32_t count);
@@ -122,7 +126,7 @@ typedef struct {
     double momentum;        /* [0, 1) */
     double weight_decay;    /* >= 0, decoupled */
     double a, b, c;         /* coefficients of a Newton-Schulz step, as above */
-    double eps;             /* > 0: floor of the Frobenius norm */
+    double eps;             /* >= 1e-30: floor of the Frobenius norm */
     double grad_scale;      /* > 0 */
     double max_norm;        /* > 0: clip to this global norm (needs norm_sq_dev); <= 0: none */
     double extra_norm_sq;   /* >= 0: other ranks' share of the squared norm */

@@ -74,6 +74,25 @@ def test_products_of_every_tile_size(m, n, k, tb):
     assert ((d.double() - want).abs() <= bound + ref.FP32 * want.abs()).all()
 
 
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("m,n,k", [(128, 270, 64), (64, 65, 128), (300, 600, 192), (70, 64, 64)])
+def test_products_with_one_operand_copied(m, n, k, tb):
+    """One operand is read where it lies, the other needs a copy, either way round, in
+    one list (the copy's place then starts where the other operand's would)."""
+    a = [rand(m, k, dtype=BF16), at_offset(rand(m, k, seed=1, dtype=BF16), 1)[0], rand(m, k, seed=2, dtype=BF16)]
+    b = [rand(*((n, k) if tb else (k, n)), seed=3 + i, dtype=BF16) for i in range(3)]
+    if tb:
+        b[0] = at_offset(b[0], 1)[0]
+    d = [torch.empty(m, n, device="cuda") for _ in range(3)]
+    lst = zs.ProductMatrices(a, b, d, transpose_b=tb)
+    ws = torch.full((zs.product_add_matrices_workspace_bytes(lst),), 0xFF, dtype=torch.uint8, device="cuda")
+    zs.product_add_matrices(lst, workspace=ws)
+    for x, y, z in zip(a, b, d):
+        y = y.t().contiguous() if tb else y
+        want = x.double() @ y.double()
+        assert ((z.double() - want).abs() <= ref.product_bound(x, y, k, 1.0, 0.0, None, False) + ref.FP32 * want.abs()).all()
+
+
 GRAMS = [(1, 1), (1, 9), (9, 1), (64, 64), (65, 70), (70, 65), (129, 300), (300, 129), (257, 64), (5, 0), (0, 4), (256, 512)]
 
 
