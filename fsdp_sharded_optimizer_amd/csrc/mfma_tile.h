@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
                  : "memory");   // M0 is not allocated: the compiler sets it before each use of its own
 }
 // All loads to LDS of this wave but the last N have arrived (of the other waves': a
-// barrier after it).
+// barrier after it).  With N > 0 no other vector memory access may come between.
 template <int N>
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
