@@ -341,7 +341,12 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
             rc = fill.flush();
             if (rc != ZS_OK) return rc;
         }
-        {
+        int64_t most_partials = 0;
+        g.each(list, [&](const Matrix& x, int64_t) {
+            most_partials = std::max(most_partials, ceil_div(x.rows * x.cols, kMomentumTile));
+            return ZS_OK;
+        });
+        if (most_partials > kPackPartials) {
             NormsBatch b;
             std::memset(&b, 0, sizeof(b));
             b.partials = partials;
@@ -375,14 +380,16 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
             b.sc_dev = sc_dev;
             b.norm_sq = norm_sq;
             b.ws = ws;
-            b.inverse = inverse;
+            b.inverse = most_partials > kPackPartials ? inverse : nullptr;
+            b.partials = partials;
             int held = 0;
             auto launch = [&](PackBatch& x, int64_t tiles) {
                 const hipError_t e = launch_pack(x, in_dtype == ZS_BF16, momentum, tiles, stream);
-                x.inverse += held;
+                if (x.inverse != nullptr) x.inverse += held;
                 held = 0;
                 return e;
             };
+            int64_t partial = 0;
             Filler<PackBatch, decltype(launch)> fill(b, launch);
             rc = g.each(list, [&](const Matrix& x, int64_t unit) -> int32_t {
                 int e = 0;
@@ -390,7 +397,8 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
                 if (failed != ZS_OK) return failed;
                 ++held;
                 b.e[e] = PackEntry{{ptr_lo(x.in), ptr_lo(x.momentum)}, ptr_hi(x.in) | ptr_hi(x.momentum) << 16,
-                                   (uint32_t)unit, (uint32_t)x.m(), x.n_tall()};
+                                   (uint32_t)unit, (uint32_t)x.m(), x.n_tall(), (uint32_t)partial};
+                partial += ceil_div(x.rows * x.cols, kMomentumTile);
                 return ZS_OK;
             });
             if (rc != ZS_OK) return rc;

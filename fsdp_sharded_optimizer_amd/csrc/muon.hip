@@ -84,16 +84,18 @@ __global__ __launch_bounds__(kBlock) void momentum_kernel(const MomentumBatch b)
     if (threadIdx.x == 0) b.partials[blockIdx.x] = total;
 }
 
+// kNsScale over a matrix's norm; a norm that is not finite makes all of it NaN
+__device__ __forceinline__ float inverse_norm(double squares, double eps) {
+    const double norm = sqrt(squares);
+    return __builtin_isfinite(norm) ? (float)((double)kNsScale / (norm > eps ? norm : eps)) : __builtin_nanf("");
+}
+
 __global__ __launch_bounds__(kBlock) void inverse_norms_kernel(const NormsBatch b) {
     const uint32_t from = b.start[blockIdx.x], to = b.start[blockIdx.x + 1];
     double s = 0.0;
     for (uint32_t i = from + threadIdx.x; i < to; i += kBlock) s += b.partials[i];
     s = block_sum(s);
-    if (threadIdx.x == 0) {
-        const double eps = b.sc_dev ? b.sc_dev->eps : b.eps, norm = sqrt(s);
-        // a norm that is not finite makes the whole matrix NaN
-        b.inverse[blockIdx.x] = __builtin_isfinite(norm) ? (float)((double)kNsScale / (norm > eps ? norm : eps)) : __builtin_nanf("");
-    }
+    if (threadIdx.x == 0) b.inverse[blockIdx.x] = inverse_norm(s, b.sc_dev ? b.sc_dev->eps : b.eps);
 }
 
 // eight consecutive elements of a row, zeros past its end
@@ -160,7 +162,17 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const PackBatch b) {
     const int64_t m = e.m, n = e.n & ~kTall, rows = tall ? n : m, cols = tall ? m : n;
     const NsPlace p(m, n);
     const uint32_t across = (uint32_t)(p.np / kSide), tile = blockIdx.x - first;
-    const float scale = b.inverse[k];
+    float scale;
+    if (b.inverse != nullptr) {
+        scale = b.inverse[k];
+    } else {
+        __shared__ float formed;
+        const int64_t count = (m * n + kMomentumTile - 1) / kMomentumTile;
+        const double s = block_sum(threadIdx.x < count ? b.partials[e.partial + threadIdx.x] : 0.0);
+        if (threadIdx.x == 0) formed = inverse_norm(s, sc.eps);
+        __syncthreads();
+        scale = formed;
+    }
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     _Float16* const hi = reinterpret_cast<_Float16*>(base + p.hi(0));
     _Float16* const lo = reinterpret_cast<_Float16*>(base + p.lo(0));

@@ -129,8 +129,19 @@ hipError_t launch_pack(const PackBatch& b, int, bool, int64_t tiles, hipStream_t
         most = std::max(most, t);
         ++seen[2][address(e.lo[0], e.hi)];
     }
-    const uint64_t at = (uint64_t)(uintptr_t)b.inverse;
-    CHECK(at >= kWs && (int64_t)(at - kWs) + (most + 1) * 4 <= ws_bytes);
+    const uint64_t at = b.inverse != nullptr ? (uint64_t)(uintptr_t)b.inverse : (uint64_t)(uintptr_t)b.partials;
+    if (b.inverse != nullptr) {
+        CHECK(at >= kWs && (int64_t)(at - kWs) + (most + 1) * 4 <= ws_bytes);
+    } else {   // from each matrix's partials, which follow one another in the table's order
+        int64_t next = b.e[0].partial;
+        for (uint32_t t = 0; t <= most; ++t) {
+            const int64_t n = ((int64_t)b.e[t].m * (b.e[t].n & ~kTall) + kMomentumTile - 1) / kMomentumTile;
+            CHECK(n <= kPackPartials && b.e[t].partial == next);
+            next += n;
+            partials_seen -= n;
+        }
+        inside((uint64_t)(uintptr_t)(b.partials + b.e[0].partial), (next - b.e[0].partial) * 8);
+    }
     for (const auto& piece : taken) CHECK(piece.second <= at);   // the norms lie behind the matrices
     return hipSuccess;
 }

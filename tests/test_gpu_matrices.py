@@ -316,6 +316,19 @@ def test_a_group_larger_than_the_shared_workspace():
         assert ref.far(b, ref.orthogonal(a)) <= ref.NS_BOUND + ref.BF16, tuple(a.shape)
 
 
+@pytest.mark.parametrize("shapes", [[(1024, 1024)], [(1024, 1025)], [(1024, 1024), (300, 40), (1024, 1025), (64, 16384), (16385, 64), (7, 9)],
+                                    [(90, 90 + i % 5) for i in range(130)] + [(64, 16384)]])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norms_of_few_and_of_many_partial_sums(shapes, dtype):
+    """Up to 2^20 elements a matrix's norm is formed where it is used, above by a launch
+    of its own, for all matrices of the call."""
+    x = [ref.matrix(r, c, i, "directions", dtype) * 2.0 ** (i % 5 - 2) for i, (r, c) in enumerate(shapes)]
+    y = [torch.empty_like(t, dtype=BF16) for t in x]
+    zs.orthogonalize_matrices(zs.OrthogonalizeMatrices(x, y))
+    for s, a, b in zip(shapes, x, y):
+        assert ref.far(b, ref.orthogonal(a)) <= ref.NS_BOUND + ref.BF16, s
+
+
 def test_same_call_same_bits():
     out = []
     for _ in range(3):
