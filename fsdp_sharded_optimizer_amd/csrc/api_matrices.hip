@@ -51,6 +51,7 @@ int32_t check_workspace(const void* ws, int64_t bytes, int64_t need) {
     if (need > 0 && (ws == nullptr || !aligned(ws, kWorkspaceAlign))) return ZS_EINVAL;
     return bytes < need ? ZS_EWORKSPACE : ZS_OK;
 }
+bool finite_float(double x) { return std::isfinite((float)x); }   // as the kernels hold it
 bool typed(const void* p, int32_t dtype) { return p != nullptr && aligned(p, (uintptr_t)elem_size(dtype)) && packable(p); }
 
 // --- products ------------------------------------------------------------------
@@ -129,7 +130,7 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
                  double alpha, double beta, void* workspace, int64_t workspace_bytes, void* hip_stream) {
     const int64_t need = products_workspace(list, count, in_dtype, flags);
     if (need < 0 || !dtype_ok(c_dtype) || !dtype_ok(d_dtype)) return ZS_EINVAL;
-    if (!std::isfinite(alpha) || !std::isfinite(beta)) return ZS_EINVAL;
+    if (!finite_float(alpha) || !finite_float(beta)) return ZS_EINVAL;
     int32_t rc = check_workspace(workspace, workspace_bytes, need);
     if (rc != ZS_OK) return rc;
     Ranges ranges;
@@ -203,7 +204,7 @@ int32_t products(const T* list, int32_t count, int32_t in_dtype, int32_t c_dtype
         const Product p = product_of(list[k], flags);
         if (p.m == 0 || p.n == 0) continue;
         const int parts = in_dtype == ZS_BF16 ? 1 : 3;
-        const void *a = p.a, *o = p.b, *c = beta == 0.0 ? nullptr : p.c;
+        const void *a = p.a, *o = p.b, *c = b.beta == 0.0f ? nullptr : p.c;
         int64_t lda = p.k, ldb = b_cols ? p.n : p.k, kp = p.k;
         if (p.k > 0) {
             const Placed q = place(p, in_dtype, at);
@@ -498,11 +499,11 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
 
 int32_t check_muon(const zs_muon* hp) {
     if (hp == nullptr) return ZS_EINVAL;
-    if (!(hp->lr >= 0.0) || !std::isfinite(hp->lr)) return ZS_EINVAL;
+    if (!(hp->lr >= 0.0) || !finite_float(hp->lr)) return ZS_EINVAL;
     if (!(hp->momentum >= 0.0 && hp->momentum < 1.0)) return ZS_EINVAL;
-    if (!(hp->weight_decay >= 0.0) || !std::isfinite(hp->weight_decay)) return ZS_EINVAL;
+    if (!(hp->weight_decay >= 0.0) || !finite_float(hp->lr * hp->weight_decay)) return ZS_EINVAL;
     if (!coefficient_ok(hp->a) || !coefficient_ok(hp->b) || !coefficient_ok(hp->c) || !eps_ok(hp->eps)) return ZS_EINVAL;
-    if (!(hp->grad_scale > 0.0) || !std::isfinite(hp->grad_scale)) return ZS_EINVAL;
+    if (!(hp->grad_scale > 0.0) || !finite_float(hp->grad_scale)) return ZS_EINVAL;
     if (std::isnan(hp->max_norm) || !(hp->extra_norm_sq >= 0.0)) return ZS_EINVAL;
     if (hp->nesterov != 0 && hp->nesterov != 1) return ZS_EINVAL;
     return hp->ns_steps >= 1 && hp->ns_steps <= ZS_NS_MAX_STEPS ? ZS_OK : ZS_EINVAL;
@@ -545,7 +546,7 @@ int32_t muon_step(const zs_muon* hp, const zs_muon_scalars* sc_dev, int32_t step
         if (n == 0) continue;
         if (!typed(x.param, param_dtype) || !typed(x.grad, grad_dtype) || !typed(x.momentum, ZS_F32)) return ZS_EINVAL;
         if (x.param_bf16 != nullptr && (param_dtype == ZS_BF16 || !typed(x.param_bf16, ZS_BF16))) return ZS_EINVAL;
-        if (!std::isfinite((float)x.scale)) return ZS_EINVAL;
+        if (!finite_float(x.scale)) return ZS_EINVAL;
         ranges.add(0, x.param, n * elem_size(param_dtype), true);
         ranges.add(1, x.grad, n * elem_size(grad_dtype), false);
         ranges.add(2, x.momentum, n * 4, true);

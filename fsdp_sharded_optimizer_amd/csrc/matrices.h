@@ -94,7 +94,7 @@ struct NsPlace {
 // A matrix whose short side is one k tile or less goes another way: all its steps
 // are polynomials of S = X X^T, a 64 x 64 matrix, so one workgroup forms their
 // product Q in fp32 from the pairs' S, and Q X is the result.  X is read twice
-// instead of ten times, in 6 launches instead of 18, and nothing is rounded to
+// instead of ten times, in 5 launches instead of 17, and nothing is rounded to
 // fp16 alone: with few singular values the roundings of the other way do not
 // average out (up to 9e-3 of a 2 x 3 matrix; this way 1e-5).
 constexpr int64_t kSkinny = kPadSide;

@@ -49,7 +49,7 @@ typedef struct {
  * product_add_matrices — d = alpha * op(a) * op(b) + beta * c for every entry of
  * a list (a preconditioner applied to gradients, with their residual).
  * bf16 inputs: products exact, summed in binary32; alpha, beta and the sum in
- * binary32, one rounding to d_dtype.  fp32 inputs are split into two bf16
+ * binary32 (finite there), one rounding to d_dtype.  fp32 inputs are split into two bf16
  * values each (16 significant bits) and three of their four products formed:
  * within 3 * 2^-16 of |a||b| per product (3e-6 of the result in the norm, as
  * measured); an input that is not finite makes what it enters NaN.  c is not
@@ -120,7 +120,8 @@ ZS_API int32_t orthogonalize_matrices(const zs_orthogonal* list, int32_t count, 
                                       double b, double c, double eps, void* workspace, int64_t workspace_bytes,
                                       void* hip_stream);
 
-/* Hyperparameters of one orthogonalised momentum step. */
+/* Hyperparameters of one orthogonalised momentum step; lr, lr * weight_decay and
+ * grad_scale finite in binary32. */
 typedef struct {
     double lr;              /* >= 0 */
     double momentum;        /* [0, 1) */

@@ -372,3 +372,16 @@ def test_lists_refuse_what_cannot_be_marshalled():
         zs.OrthogonalizeMatrices([x], [torch.zeros(2, 8)])
     with pytest.raises(ValueError):
         zs.MuonMatrices([x], [x], [x], scale=[1.0, 2.0])
+
+
+def test_scalars_beyond_the_kernels_range_are_refused():
+    """Finite in binary64 and infinite in the binary32 that the kernels hold."""
+    rows, grams = [[FAKE, FAKE + MIB, 0, FAKE + 2 * MIB, 64, 64, 64]], [[FAKE, 0, FAKE + MIB, 64, 64, 0, 0]]
+    for kw in (dict(alpha=1e39), dict(alpha=-1e300), dict(beta=1e39)):
+        assert product(rows, **kw) == B.ZS_EINVAL and gram(grams, **kw) == B.ZS_EINVAL, kw
+    out = M.MuonScalars()
+    for kw in (dict(lr=1e39), dict(grad_scale=1e39), dict(lr=1e20, weight_decay=1e20), dict(weight_decay=float("inf")),
+               dict(weight_decay=float("nan"))):
+        assert muon(muons(), h=hp_with(**kw)) == B.ZS_EINVAL, kw
+        assert L.muon_scalars(hp_with(**kw), ctypes.byref(out)) == B.ZS_EINVAL, kw
+    assert L.muon_scalars(hp_with(lr=1e38, weight_decay=1.0), ctypes.byref(out)) == B.ZS_OK
