@@ -134,6 +134,24 @@ def test_grams_of_larger_tiles():
         assert torch.equal(d, d.t())
 
 
+@pytest.mark.parametrize("dtype,tb", [(BF16, False), (BF16, True), (F32, False), (F32, True)])
+def test_products_beyond_32_bits(dtype, tb):
+    """The longest k, and operands of more bytes than 32 bits address."""
+    m, n, k = 9, 2040, 1 << 20
+    a, b = rand(m, k, seed=1, dtype=dtype), rand(*((n, k) if tb else (k, n)), seed=2, dtype=dtype)
+    d = torch.empty(m, n, dtype=F32, device="cuda")
+    zs.product_add_matrices(zs.ProductMatrices([a], [b], [d], transpose_b=tb))
+    want = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    for at in range(0, k, k // 16):
+        y = b[:, at:at + k // 16].t().contiguous() if tb else b[at:at + k // 16]
+        want += a[:, at:at + k // 16].double() @ y.double()
+    # An addition is off by 2^-24 of the running sum at most, and that is no larger, rms, than
+    # the result: k errors (3 k of split inputs) of either sign add up to sqrt(k) of one.  A
+    # split product is off by 3 * 2^-16 of itself at most; their errors add up as the products do.
+    split = dtype == F32
+    assert ref.far(d, want) <= ((3 if split else 1) * k) ** 0.5 * ref.FP32 + (3 * 2.0 ** -16 if split else 0.0)
+
+
 def test_products_of_non_finite_inputs():
     """An infinity or NaN stays in its row and column; masked out by beta = 0 in c."""
     a, b = rand(70, 100, dtype=BF16), rand(100, 90, seed=1, dtype=BF16)
@@ -314,6 +332,15 @@ def test_a_group_larger_than_the_shared_workspace():
     zs.orthogonalize_matrices(lst, workspace=ws)
     for a, b in zip(x, y):
         assert ref.far(b, ref.orthogonal(a)) <= ref.NS_BOUND + ref.BF16, tuple(a.shape)
+
+
+@pytest.mark.parametrize("shape", [(2040, 1 << 20), (1 << 20, 2040), (46300, 46300 // 64)])
+def test_orthogonalize_beyond_32_bits(shape):
+    """The longest sides, and more bytes than 32 bits address."""
+    x = rand(*shape, seed=5, dtype=BF16)
+    y = torch.empty_like(x)
+    zs.orthogonalize_matrices(zs.OrthogonalizeMatrices([x], [y]))
+    assert ref.far(y, ref.orthogonal(x)) <= ref.NS_BOUND + ref.BF16
 
 
 @pytest.mark.parametrize("shapes", [[(1024, 1024)], [(1024, 1025)], [(1024, 1024), (300, 40), (1024, 1025), (64, 16384), (16385, 64), (7, 9)],
