@@ -518,7 +518,8 @@ __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatc
         }
         __syncthreads();
     }
-    // the scale: Q's largest magnitude to [2^12, 2^13)
+    // the scale: Q's largest magnitude to [2^12, 2^13), by a power of two that binary32 has
+    // (2^127 at most: a Q below 2^-115 stays smaller)
     float most = 0.0f;
     for (int i = threadIdx.x; i < kSkinny * kSkinny; i += kStepThreads)
         most = fmaxf(most, fabsf(q.v[i / kSkinny * kPitch + i % kSkinny]));
@@ -531,6 +532,7 @@ __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatc
     for (int w = 0; w < kStepThreads / 64; ++w) most = fmaxf(most, t.v[w]);
     int exponent = 0;
     if (most > 0.0f && __builtin_isfinite(most)) (void)frexpf(most, &exponent);
+    exponent = max(exponent, 13 - 127);
     const float scale = ldexpf(1.0f, 13 - exponent);
     _Float16* const out = reinterpret_cast<_Float16*>(base + p.q());
     for (int i = threadIdx.x; i < kSkinny * kSkinny; i += kStepThreads) {
