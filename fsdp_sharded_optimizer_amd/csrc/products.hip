@@ -479,11 +479,14 @@ __device__ __forceinline__ void square_product(const Square& x, const Square& y,
 
 // Q = M_1 M_2 ... with M = a I + b S + c S^2 and S <- M S M after each (all
 // polynomials of the first S: they commute), and Q as two fp16 values times a power
-// of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].
+// of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].  I has the
+// matrix's own rows alone: a^steps in the padding would be most of Q's largest value,
+// to which its scale goes (3.4445^20 = 5e10), and leave its other values few bits or none.
 __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatch b) {
     __shared__ Square s, t, m, q;
     const NsEntry e = b.e[blockIdx.x];
     const SkinnyPlace p(e.n);
+    const int rows = (int)e.m;
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const float ca = b.sc_dev ? b.sc_dev->a : b.a, cb = b.sc_dev ? b.sc_dev->b : b.b, cc = b.sc_dev ? b.sc_dev->c : b.c;
     const float* const parts = reinterpret_cast<const float*>(base + p.parts());
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatc
     for (int step = 0; step < b.steps; ++step) {
         square_product(s, s, [&](int r, int c, float x) {
             const int at = r * kPitch + c;
-            m.v[at] = (s.v[at] * cb + x * cc) + (r == c ? ca : 0.0f);
+            m.v[at] = (s.v[at] * cb + x * cc) + (r == c && r < rows ? ca : 0.0f);
             if (step == 0) q.v[at] = m.v[at];
         });
         __syncthreads();

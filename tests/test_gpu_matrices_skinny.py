@@ -25,3 +25,14 @@ def test_a_polynomial_that_nearly_vanishes(coefficients, steps):
     x = [ref.matrix(r, c, 7) for r, c in ((64, 200), (90, 8), (1, 30), (64, 64))]
     for a, b in zip(x, orthogonalized(x, steps, coefficients)):
         assert ref.far(b, ref.orthogonal(a, steps, coefficients)) <= ref.NS_BOUND + ref.BF16, tuple(a.shape)
+
+
+@pytest.mark.parametrize("steps,coefficients", [(16, ref.COEFFICIENTS), (20, ref.COEFFICIENTS), (32, ref.COEFFICIENTS),
+                                                (20, (1.5, -0.5, 0.0)), (32, (1.875, -1.25, 0.375))])
+def test_many_steps_of_fewer_rows_than_a_tile(steps, coefficients):
+    """Well-conditioned matrices: a step multiplies what the steps before it were off by by 0.7
+    to 3.4 and, over all of them, the errors of single steps add up to less than 1000 of one
+    (first order, from the singular values); a step's few roundings are 2^-22 each: 1e-3."""
+    x = [ref.matrix(r, c, 3) for r, c in ((1, 100), (100, 1), (8, 100), (100, 8), (63, 500), (500, 63))]
+    for a, b in zip(x, orthogonalized(x, steps, coefficients)):
+        assert ref.far(b, ref.orthogonal(a, steps, coefficients)) <= ref.NS_BOUND + ref.BF16, tuple(a.shape)
