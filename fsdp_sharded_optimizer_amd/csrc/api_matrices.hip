@@ -415,7 +415,6 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
         b.a = sc.a;
         b.b = sc.b;
         b.c = sc.c;
-        b.steps = steps;
         TileCount square, wide;
         int64_t skinny = 0, others = 0;
         g.each(list, [&](const Matrix& x, int64_t) {
@@ -457,7 +456,9 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
                 if (rc != ZS_OK) return rc;
             }
         }
-        if (skinny > 0) {
+        for (int32_t done = 0; done < steps && skinny > 0; done += kSkinnySteps) {
+            b.which = done > 0;
+            b.steps = std::min(steps - done, kSkinnySteps);
             rc = phase(true, [&](const Matrix& x) { return SkinnyPlace(x.n()).chunks; },
                        [&](const NsBatch& x, int64_t tiles) { return launch_skinny_gram(x, tiles, stream); });
             if (rc != ZS_OK) return rc;

@@ -91,13 +91,25 @@ struct NsPlace {
     __host__ __device__ __forceinline__ int64_t poly() const { return 4 * x + mp * mp * 2; }
     __host__ __device__ __forceinline__ int64_t bytes() const { return 4 * x + 2 * mp * mp * 2; }
 };
-// A matrix whose short side is one k tile or less goes another way: all its steps
+// A matrix whose short side is one k tile or less goes another way: its steps
 // are polynomials of S = X X^T, a 64 x 64 matrix, so one workgroup forms their
 // product Q in fp32 from the pairs' S, and Q X is the result.  X is read twice
 // instead of ten times, in 5 launches instead of 17, and nothing is rounded to
 // fp16 alone: with few singular values the roundings of the other way do not
 // average out (up to 9e-3 of a 2 x 3 matrix; this way 1e-5).
+// That holds for a few steps at a time.  S is off by 2^-23 of its largest value, and
+// its small and null values, that error with them, grow by a^2 a step, below zero too,
+// where the polynomial has no bound (3.4445: a 64 x 256 matrix of rank 8 off by 1e-4 after
+// 5 steps, 0.4 after 8, NaN after 12).  And Q, a pair, is off by 2^-22 of its own largest
+// value, a^steps there.  So X becomes Q X, and S is formed anew from it, before |a|^steps
+// passes kSkinnyGrowth, and after kSkinnySteps steps (with them Q is off by 1.2e-4 at
+// most, S by 512^2 / a^2 2^-23 = 3e-3 of what X is off the small values by).  After
+// kSkinnySteps every workgroup of the next sum of S does so for its columns (a launch that
+// only the number of steps decides on: a captured step's coefficients may change); within them,
+// for a above 3.48, the workgroup that forms Q, for all columns.
 constexpr int64_t kSkinny = kPadSide;
+constexpr int32_t kSkinnySteps = 5;
+constexpr float kSkinnyGrowth = 512.0f;
 // Its place: X's first values, second values and first values again (together the
 // 192 x np right operand of Q X), the partial sums of S, Q as its left operand
 // (64 x 192), Q's scale.
@@ -130,13 +142,13 @@ struct NsBatch {
     char* ws;
     const MuonScalars* sc_dev;
     float a, b, c;         // unless sc_dev is set
-    int32_t which;         // the X that is read
-    int32_t steps;         // skinny matrices: of them all
+    int32_t which;         // the X that is read; skinny matrices: 1 where X is to become Q X first
+    int32_t steps;         // skinny matrices: up to the next sum of S
 };
 static_assert(sizeof(NsBatch) <= 4096, "kernel arguments");
 enum NsPhase : int { kNsGram = 0, kNsPoly = 1, kNsUpdate = 2 };
 hipError_t launch_ns(const NsBatch& b, int phase, int size, int64_t tiles, hipStream_t stream);
-// a workgroup per partial sum of S; a workgroup per matrix
+// a workgroup per partial sum of S (after X <- Q X where b.which is 1); a workgroup per matrix
 hipError_t launch_skinny_gram(const NsBatch& b, int64_t tiles, hipStream_t stream);
 hipError_t launch_skinny_steps(const NsBatch& b, int64_t count, hipStream_t stream);
 

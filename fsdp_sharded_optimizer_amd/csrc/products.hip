@@ -424,8 +424,21 @@ __global__ __launch_bounds__(T::kThreads, 2) void ns_final_kernel(const FinalBat
 
 // --- matrices whose short side is at most 64 -------------------------------------
 
+// Columns [n0, n0 + 64) of Q X, in units of skinny_scale.
+__device__ __forceinline__ void skinny_product(const char* base, const SkinnyPlace& p, int n0, f32x4 (&acc)[T64::MI][T64::NI]) {
+    const Operand q = by_rows(reinterpret_cast<const uint16_t*>(base + p.q()), 3 * kSkinny, (int)kSkinny);
+    const Operand x = blocked_by_columns(reinterpret_cast<const uint16_t*>(base), (int)(p.np / 64), (int)p.np);
+    multiply<T64, false, true>(q, x, 0, n0, 3, tile_lds<T64>(), acc);
+}
+__device__ __forceinline__ float skinny_scale(const char* base, const SkinnyPlace& p) {
+    return *reinterpret_cast<const float*>(base + p.scale());
+}
+
 // One partial sum of S from the pairs: hi hi^T + hi lo^T + lo hi^T (the fourth
-// product is below fp32's last bit).
+// product is below fp32's last bit).  APPLY: of Q X, which takes X's place: a workgroup
+// reads and writes its own columns alone, 64 at a time, all of them in LDS before the
+// first is written.
+template <bool APPLY>
 __global__ __launch_bounds__(T64::kThreads, 2) void skinny_gram_kernel(const NsBatch b) {
     uint32_t first;
     const NsEntry e = b.e[find_tensor(b.tab, blockIdx.x, first)];
@@ -433,8 +446,36 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_gram_kernel(const NsB
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const int64_t chunk = blockIdx.x - first, from = chunk * p.chunk, left = p.np / kTileK - from;
     const int tiles = (int)(left < p.chunk ? left : p.chunk);
-    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base) + from * kBlockElems;
     const int across = (int)(p.np / 64);
+    if constexpr (APPLY) {
+        const float scale = skinny_scale(base, p) * kNsScale;
+        _Float16* const x0 = reinterpret_cast<_Float16*>(base);
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const int n0 = (int)(from + t) * T64::BN;
+            f32x4 acc[T64::MI][T64::NI];
+            skinny_product(base, p, n0, acc);
+            each_row<T64, true>(acc, 0, n0, [&](int r, int c, const float (&x)[8]) {
+                const int64_t at = blocked(r, c, across);
+                f16x8 h, l;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    _Float16 y, z;
+                    split_f16(x[j] * scale, y, z);
+                    h[j] = y;
+                    l[j] = z;
+                }
+                *reinterpret_cast<f16x8*>(x0 + at) = h;
+                *reinterpret_cast<f16x8*>(x0 + p.x / 2 + at) = l;
+                *reinterpret_cast<f16x8*>(x0 + p.x + at) = h;
+            });
+        }
+        // what the other waves stored is read below
+        loads_done<0>();
+        __threadfence_block();
+        __syncthreads();
+    }
+    const uint16_t* const x = reinterpret_cast<const uint16_t*>(base) + from * kBlockElems;
     const Operand hi = blocked_by_rows(x, across, (int)kSkinny), lo = blocked_by_rows(x + p.x / 2, across, (int)kSkinny);
     f32x4 sum[T64::MI][T64::NI], acc[T64::MI][T64::NI];
     multiply<T64, false, false>(hi, lo, 0, 0, tiles, tile_lds<T64>(), sum);
@@ -477,16 +518,104 @@ __device__ __forceinline__ void square_product(const Square& x, const Square& y,
     for (int i = 0; i < 4; ++i) f(row + 4 * kl + i, col + at, acc[0][i] + acc[1][i]);
 }
 
-// Q = M_1 M_2 ... with M = a I + b S + c S^2 and S <- M S M after each (all
-// polynomials of the first S: they commute), and Q as two fp16 values times a power
-// of two, in the form of Q X's left operand: [hi | hi / kNsLow | lo].  I has the
-// matrix's own rows alone: a^steps in the padding would be most of Q's largest value,
-// to which its scale goes (3.4445^20 = 5e10), and leave its other values few bits or none.
+// acc += y y^T, as square_product forms it.
+__device__ __forceinline__ void add_square(const Square& y, f32x4 (&acc)[2]) {
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, row = wave / 4 * 16, col = wave % 4 * 16, at = l & 15, kl = l >> 4;
+#pragma unroll
+    for (int k = 0; k < kSkinny; k += 8)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(y.v[(row + at) * kPitch + k + 4 * h + kl],
+                                                          y.v[(col + at) * kPitch + k + 4 * h + kl], acc[h], 0, 0, 0);
+}
+// f(row, column) of this lane's four results of those
+template <class F>
+__device__ __forceinline__ void each_result(F&& f) {
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f(i, wave / 4 * 16 + 4 * (l >> 4) + i, wave % 4 * 16 + (l & 15));
+}
+
+// Q = M_1 M_2 ... of `steps` steps with M = a I + b S + c S^2 and S <- M S M after each
+// (all polynomials of the first S: they commute).  I has the matrix's own rows
+// alone: a^steps in the padding would be most of Q's largest value, to which its scale
+// goes (3.4445^20 = 5e10), and leave its other values few bits or none.
+__device__ __forceinline__ void polynomials(Square& s, Square& t, Square& m, Square& q, int rows, int steps, float ca, float cb,
+                                            float cc) {
+    for (int step = 0; step < steps; ++step) {
+        square_product(s, s, [&](int r, int c, float x) {
+            const int at = r * kPitch + c;
+            m.v[at] = (s.v[at] * cb + x * cc) + (r == c && r < rows ? ca : 0.0f);
+            if (step == 0) q.v[at] = m.v[at];
+        });
+        __syncthreads();
+        const bool more = step + 1 < steps;
+        if (step > 0) {
+            // q's own product: kept until every wave has read q
+            f32x4 kept;
+            int n = 0;
+            square_product(m, q, [&](int, int, float x) { kept[n++] = x; });
+            __syncthreads();
+            each_result([&](int i, int r, int c) { q.v[r * kPitch + c] = kept[i]; });
+        }
+        if (more) {
+            square_product(m, s, [&](int r, int c, float x) { t.v[r * kPitch + c] = x; });
+            __syncthreads();
+            square_product(t, m, [&](int r, int c, float x) { s.v[r * kPitch + c] = x; });
+        }
+        __syncthreads();
+    }
+}
+
+// X <- Q X and S anew, by one workgroup: 64 columns at a time in LDS, every
+// thread the same four elements of them.  There may be 2^20 columns: the sums of every
+// 1024 are added in binary64.
+__device__ __forceinline__ void apply_alone(char* base, const SkinnyPlace& p, const Square& q, Square& s, Square& t, Square& m) {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    const int own = threadIdx.x * 4, place = own / (int)kSkinny * kPitch + own % (int)kSkinny;
+    const int blocks = (int)(p.np / kSkinny);
+    double total[4] = {0.0, 0.0, 0.0, 0.0};
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll 1
+    for (int k = 0; k < blocks; ++k) {
+        _Float16* const hi = reinterpret_cast<_Float16*>(base) + (int64_t)k * kBlockElems + own;
+        _Float16 *const lo = hi + p.x / 2, *const again = hi + p.x;
+        f16x4 h = *reinterpret_cast<const f16x4*>(hi), l = *reinterpret_cast<const f16x4*>(lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.v[place + j] = __builtin_fmaf((float)l[j], 1.0f / kNsLow, (float)h[j]);
+        __syncthreads();
+        square_product(q, t, [&](int r, int c, float x) { m.v[r * kPitch + c] = x; });
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            _Float16 y, z;
+            split_f16(m.v[place + j], y, z);
+            h[j] = y;
+            l[j] = z;
+            m.v[place + j] = __builtin_fmaf((float)z, 1.0f / kNsLow, (float)y);
+        }
+        *reinterpret_cast<f16x4*>(hi) = h;
+        *reinterpret_cast<f16x4*>(lo) = l;
+        *reinterpret_cast<f16x4*>(again) = h;
+        __syncthreads();
+        add_square(m, acc);   // (the next m is written two barriers on)
+        if (k % 16 == 15 || k + 1 == blocks) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[i] += (double)acc[0][i] + (double)acc[1][i];
+            acc[0] = acc[1] = f32x4{0, 0, 0, 0};
+        }
+    }
+    each_result([&](int i, int r, int c) { s.v[r * kPitch + c] = (float)(total[i] * (1.0 / (kNsScale * kNsScale))); });
+    __syncthreads();
+}
+
+// The product Q of b.steps steps' polynomials, as two fp16 values times a power of two, in
+// the form of Q X's left operand: [hi | hi / kNsLow | lo].  Where they are too many for
+// one product (kSkinnyGrowth), of the last ones, X having become what the others make of it.
 __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatch b) {
     __shared__ Square s, t, m, q;
     const NsEntry e = b.e[blockIdx.x];
     const SkinnyPlace p(e.n);
-    const int rows = (int)e.m;
     char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const float ca = b.sc_dev ? b.sc_dev->a : b.a, cb = b.sc_dev ? b.sc_dev->b : b.b, cc = b.sc_dev ? b.sc_dev->c : b.c;
     const float* const parts = reinterpret_cast<const float*>(base + p.parts());
@@ -496,31 +625,15 @@ __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatc
         s.v[i / kSkinny * kPitch + i % kSkinny] = x * (1.0f / (kNsScale * kNsScale));
     }
     __syncthreads();
-    for (int step = 0; step < b.steps; ++step) {
-        square_product(s, s, [&](int r, int c, float x) {
-            const int at = r * kPitch + c;
-            m.v[at] = (s.v[at] * cb + x * cc) + (r == c && r < rows ? ca : 0.0f);
-            if (step == 0) q.v[at] = m.v[at];
-        });
-        __syncthreads();
-        const bool more = step + 1 < b.steps;
-        if (step > 0) {
-            // q's own product: kept until every wave has read q
-            f32x4 kept;
-            int n = 0;
-            square_product(m, q, [&](int, int, float x) { kept[n++] = x; });
-            __syncthreads();
-            const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q.v[(wave / 4 * 16 + 4 * (l >> 4) + i) * kPitch + wave % 4 * 16 + (l & 15)] = kept[i];
-        }
-        if (more) {
-            square_product(m, s, [&](int r, int c, float x) { t.v[r * kPitch + c] = x; });
-            __syncthreads();
-            square_product(t, m, [&](int r, int c, float x) { s.v[r * kPitch + c] = x; });
-        }
-        __syncthreads();
+    const float slope = fabsf(ca);
+    int at_once = 1;
+    for (float grown = slope * slope; at_once < b.steps && grown <= kSkinnyGrowth; grown *= slope) ++at_once;
+    int left = b.steps;
+    for (; left > at_once; left -= at_once) {
+        polynomials(s, t, m, q, (int)e.m, at_once, ca, cb, cc);
+        apply_alone(base, p, q, s, t, m);
     }
+    polynomials(s, t, m, q, (int)e.m, left, ca, cb, cc);
     // the scale: Q's largest magnitude to [2^12, 2^13), by a power of two that binary32 has
     // (2^127 at most: a Q below 2^-115 stays smaller)
     float most = 0.0f;
@@ -560,11 +673,9 @@ __global__ __launch_bounds__(T64::kThreads, 2) void skinny_final_kernel(const Fi
     const SkinnyPlace p(to.n);
     const char* const base = b.ws + (int64_t)e.base * kNsUnit;
     const int n0 = (int)(blockIdx.x - first) * T64::BN;
-    const Operand q = by_rows(reinterpret_cast<const uint16_t*>(base + p.q()), 3 * kSkinny, (int)kSkinny);
-    const Operand x = blocked_by_columns(reinterpret_cast<const uint16_t*>(base), (int)(p.np / 64), (int)p.np);
     f32x4 acc[T64::MI][T64::NI];
-    multiply<T64, false, true>(q, x, 0, n0, 3, tile_lds<T64>(), acc);
-    const float scale = *reinterpret_cast<const float*>(base + p.scale());
+    skinny_product(base, p, n0, acc);
+    const float scale = skinny_scale(base, p);
     if (to.tall) to.template columns<T64, true>(acc, 0, n0, scale);
     else each_row<T64, true>(acc, 0, n0, [&](int r, int c, float (&x)[8]) { to.row(r, c, x, scale); });
 }
@@ -612,7 +723,9 @@ hipError_t launch_ns(const NsBatch& b, int phase, int size, int64_t tiles, hipSt
 }
 
 hipError_t launch_skinny_gram(const NsBatch& b, int64_t tiles, hipStream_t stream) {
-    hipLaunchKernelGGL(skinny_gram_kernel, dim3((unsigned)tiles), dim3(T64::kThreads), 0, stream, b);
+    const dim3 grid((unsigned)tiles), block(T64::kThreads);
+    if (b.which) hipLaunchKernelGGL((skinny_gram_kernel<true>), grid, block, 0, stream, b);
+    else hipLaunchKernelGGL((skinny_gram_kernel<false>), grid, block, 0, stream, b);
     return hipGetLastError();
 }
 

@@ -109,7 +109,10 @@ typedef struct {
  * usual coefficients (3.4445, -4.775, 2.0315) and 5 steps, and their rounding to
  * bf16 (2^-8 of a value at most, 1.7e-3 in the norm) comes on top.  Where the
  * short side is 64 or less nothing is held in fp16 alone (the polynomials of S are
- * formed in binary32 and applied to the pair): 1e-6 to 2e-4.
+ * formed in binary32, of at most 5 steps at a time, and applied to the pair): 1e-6 to
+ * 4e-4.  More steps multiply what the first ones were off by as they multiply the
+ * matrix: singular values below 2^-22 of the largest are what roundings left there, and
+ * grow by a each step until the polynomial holds them.
  * A zero matrix gives zeros, one with a value that is not finite NaN.  steps: 1 to
  * ZS_NS_MAX_STEPS; |a|, |b|, |c| at most 32 and such that X stays bounded (fp16 ends
  * at 255 times the scale); eps: at least 1e-30.
