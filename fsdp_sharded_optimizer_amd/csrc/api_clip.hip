@@ -41,7 +41,7 @@ int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count, doubl
                               double* out_sq_dev, void* workspace, int64_t workspace_bytes, void* hip_stream) {
     const int64_t parts = mixed_partials(grads, count);
     if (parts < 0 || out_sq_dev == nullptr || !aligned(out_sq_dev, 8) || !aligned(norms_sq_dev, 8)) return ZS_EINVAL;
-    if (!(grad_scale > 0.0) || !std::isfinite(grad_scale)) return ZS_EINVAL;
+    if (!positive_float(grad_scale)) return ZS_EINVAL;
     const int64_t need = grad_norms_sq_tensors_workspace_bytes(grads, count);
     if (need > 0 && (workspace == nullptr || !aligned(workspace, 8))) return ZS_EINVAL;
     if (workspace_bytes < need) return ZS_EWORKSPACE;
@@ -117,7 +117,7 @@ int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count, doubl
 int32_t grad_clip_tensors(const zs_mixed_tensor* grads, const zs_mixed_tensor* out, int32_t count, double grad_scale,
                           double max_norm, double extra_norm_sq, const double* norm_sq_dev, void* hip_stream) {
     if (mixed_partials(grads, count) < 0 || mixed_partials(out, count) < 0) return ZS_EINVAL;
-    if (!(grad_scale > 0.0) || !std::isfinite(grad_scale)) return ZS_EINVAL;
+    if (!positive_float(grad_scale)) return ZS_EINVAL;
     if (std::isnan(max_norm) || !(extra_norm_sq >= 0.0) || !aligned(norm_sq_dev, 8)) return ZS_EINVAL;
     Ranges ranges;
     if (!ranges.reserve(count, 2)) return ZS_EINVAL;

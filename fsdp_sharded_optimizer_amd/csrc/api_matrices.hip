@@ -51,7 +51,6 @@ int32_t check_workspace(const void* ws, int64_t bytes, int64_t need) {
     if (need > 0 && (ws == nullptr || !aligned(ws, kWorkspaceAlign))) return ZS_EINVAL;
     return bytes < need ? ZS_EWORKSPACE : ZS_OK;
 }
-bool finite_float(double x) { return std::isfinite((float)x); }   // as the kernels hold it
 bool typed(const void* p, int32_t dtype) { return p != nullptr && aligned(p, (uintptr_t)elem_size(dtype)) && packable(p); }
 
 // --- products ------------------------------------------------------------------
@@ -504,7 +503,7 @@ int32_t check_muon(const zs_muon* hp) {
     if (!(hp->momentum >= 0.0 && hp->momentum < 1.0)) return ZS_EINVAL;
     if (!(hp->weight_decay >= 0.0) || !finite_float(hp->lr * hp->weight_decay)) return ZS_EINVAL;
     if (!coefficient_ok(hp->a) || !coefficient_ok(hp->b) || !coefficient_ok(hp->c) || !eps_ok(hp->eps)) return ZS_EINVAL;
-    if (!(hp->grad_scale > 0.0) || !finite_float(hp->grad_scale)) return ZS_EINVAL;
+    if (!positive_float(hp->grad_scale)) return ZS_EINVAL;
     if (std::isnan(hp->max_norm) || !(hp->extra_norm_sq >= 0.0)) return ZS_EINVAL;
     if (hp->nesterov != 0 && hp->nesterov != 1) return ZS_EINVAL;
     return hp->ns_steps >= 1 && hp->ns_steps <= ZS_NS_MAX_STEPS ? ZS_OK : ZS_EINVAL;

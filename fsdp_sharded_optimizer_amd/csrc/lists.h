@@ -153,6 +153,10 @@ private:
     int64_t tiles_ = 0;
 };
 
+// Scalars as the kernels hold them, in binary32
+inline bool finite_float(double x) { return std::isfinite((float)x); }
+inline bool positive_float(double x) { return (float)x > 0.0f && finite_float(x); }
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <typename T>

@@ -124,7 +124,7 @@ ZS_API int32_t orthogonalize_matrices(const zs_orthogonal* list, int32_t count, 
                                       void* hip_stream);
 
 /* Hyperparameters of one orthogonalised momentum step; lr, lr * weight_decay and
- * grad_scale finite in binary32. */
+ * grad_scale finite in binary32, grad_scale not 0 there either. */
 typedef struct {
     double lr;              /* >= 0 */
     double momentum;        /* [0, 1) */

@@ -67,7 +67,8 @@ typedef struct {
  * (*out_sq_dev, the norm_sq_dev of the steps and of grad_clip_tensors).  As
  * grad_norm_sq_tensors, with squares exact in binary64 and summed in binary64
  * in a fixed order that depends only on the numels and dtypes; a tensor without
- * elements has the norm 0, an empty list writes 0.
+ * elements has the norm 0, an empty list writes 0.  grad_scale: positive and finite
+ * in binary32.
  * grads: read; norms_sq_dev: `count` device doubles, written; out_sq_dev: device
  * double, written; workspace: device, 8-byte aligned, at least
  * grad_norms_sq_tensors_workspace_bytes bytes (host only; -1 for an invalid
@@ -85,9 +86,9 @@ ZS_API int32_t grad_norms_sq_tensors(const zs_mixed_tensor* grads, int32_t count
  * out[k] = fl32(fl32(widen(grads[k]) * (float)grad_scale) * coef), rounded to out[k]'s
  * dtype, with adamw_step's coef: 1 where norm_sq_dev is NULL or max_norm <= 0, else
  * (float)min(1, max_norm / (sqrt(*norm_sq_dev + extra_norm_sq) + 1e-6)).  Where that sum is not
- * finite nothing is written.  out[k] has grads[k]'s numel and either dtype; it may
- * be grads[k] itself in the same dtype (in place), and shares no byte with
- * another buffer of the call otherwise.
+ * finite nothing is written.  grad_scale: positive and finite in binary32.  out[k] has
+ * grads[k]'s numel and either dtype; it may be grads[k] itself in the same dtype (in
+ * place), and shares no byte with another buffer of the call otherwise.
  * Errors: ZS_EINVAL, ZS_EOVERLAP, ZS_EHIP.
  */
 ZS_API int32_t grad_clip_tensors(const zs_mixed_tensor* grads, const zs_mixed_tensor* out, int32_t count,

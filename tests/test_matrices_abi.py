@@ -385,3 +385,15 @@ def test_scalars_beyond_the_kernels_range_are_refused():
         assert muon(muons(), h=hp_with(**kw)) == B.ZS_EINVAL, kw
         assert L.muon_scalars(hp_with(**kw), ctypes.byref(out)) == B.ZS_EINVAL, kw
     assert L.muon_scalars(hp_with(lr=1e38, weight_decay=1.0), ctypes.byref(out)) == B.ZS_OK
+
+
+def test_grad_scales_that_binary32_does_not_hold_are_refused():
+    """The kernels multiply by the binary32 value: an infinite one would write inf and NaN over
+    the gradients, one that is 0 there would erase them."""
+    grads = fill(T.MixedTensor, [[FAKE, 5000, 0, 0]])
+    for scale in (1e39, 1e300, 1e-46, 1e-60, 5e-324):
+        assert L.grad_clip_tensors(grads, grads, 1, scale, 0.0, 0.0, None, None) == B.ZS_EINVAL
+        assert L.grad_norms_sq_tensors(grads, 1, scale, None, FAKE + MIB, FAKE + 2 * MIB, MIB, None) == B.ZS_EINVAL
+        with pytest.raises(zs.ZShardError):
+            zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, grad_scale=scale))
+    zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, grad_scale=1e-45))     # a subnormal one is held
