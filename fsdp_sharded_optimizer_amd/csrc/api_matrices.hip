@@ -500,7 +500,7 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
 int32_t check_muon(const zs_muon* hp) {
     if (hp == nullptr) return ZS_EINVAL;
     if (!(hp->lr >= 0.0) || !finite_float(hp->lr)) return ZS_EINVAL;
-    if (!(hp->momentum >= 0.0 && hp->momentum < 1.0)) return ZS_EINVAL;
+    if (!(hp->momentum >= 0.0 && (float)hp->momentum < 1.0f)) return ZS_EINVAL;
     if (!(hp->weight_decay >= 0.0) || !finite_float(hp->lr * hp->weight_decay)) return ZS_EINVAL;
     if (!coefficient_ok(hp->a) || !coefficient_ok(hp->b) || !coefficient_ok(hp->c) || !eps_ok(hp->eps)) return ZS_EINVAL;
     if (!positive_float(hp->grad_scale)) return ZS_EINVAL;

@@ -127,7 +127,7 @@ ZS_API int32_t orthogonalize_matrices(const zs_orthogonal* list, int32_t count, 
  * grad_scale finite in binary32, grad_scale not 0 there either. */
 typedef struct {
     double lr;              /* >= 0 */
-    double momentum;        /* [0, 1) */
+    double momentum;        /* [0, 1), in binary32 too */
     double weight_decay;    /* >= 0, decoupled */
     double a, b, c;         /* coefficients of a Newton-Schulz step, as above */
     double eps;             /* >= 1e-30: floor of the Frobenius norm */

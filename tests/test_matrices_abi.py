@@ -397,3 +397,12 @@ def test_grad_scales_that_binary32_does_not_hold_are_refused():
         with pytest.raises(zs.ZShardError):
             zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, grad_scale=scale))
     zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, grad_scale=1e-45))     # a subnormal one is held
+
+
+def test_a_momentum_that_is_one_in_binary32_is_refused():
+    """Beside 1 - momentum, formed in binary64, it would never forget a gradient."""
+    for momentum in (1.0 - 2.0 ** -26, 1.0 - 2.0 ** -53):
+        with pytest.raises(zs.ZShardError):
+            zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, momentum=momentum))
+    sc = M.MuonScalars.from_buffer_copy(zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, momentum=1.0 - 2.0 ** -24)))
+    assert sc.momentum == 1.0 - 2.0 ** -24 and sc.one_minus_momentum == 2.0 ** -24
