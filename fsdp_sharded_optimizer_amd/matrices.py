@@ -279,8 +279,11 @@ class MuonMatrices(_MatrixList):
                       (torch.bfloat16,), optional=True)
         for field, i in (("rows", 0), ("cols", 1)):
             self._fill(field, [s[i] for s in self.shapes])
-        self._fill("scale", [update_scale(*(p.shape[-2:]), s) for p, s in zip(params, scales)
-                             for _ in range(1 if p.dim() == 2 else p.shape[0])])
+        factors = [update_scale(*(p.shape[-2:]), s) for p, s in zip(params, scales)
+                   for _ in range(1 if p.dim() == 2 else p.shape[0])]
+        if not all(math.isfinite(_F(s).value) for s in factors):
+            raise ValueError("scale: finite values, in binary32 too")
+        self._fill("scale", factors)
 
     def set_grads(self, grads) -> None:
         """Other gradients of the same shapes (fp32 or bf16, one dtype)."""

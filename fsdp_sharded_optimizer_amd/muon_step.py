@@ -109,11 +109,15 @@ class MuonOptimizer:
         if self._grads is None:
             raise RuntimeError("step() without gradients")
         self._check_clip(norm_sq)
+        configs = [self._hp(decay, extra_norm_sq) for decay, _, _ in self._groups]
+        if len(configs) > 1:   # what one call would refuse is refused before another has run
+            for hp in configs:
+                zm.muon_scalars_bytes(hp)
         norm = norm_sq
         if norm is None and self.compute_norm:
             norm = zt.grad_norm_sq_tensors(self._grads, self.grad_scale, self.norm_sq, self._workspace)
-        for decay, _, lst in self._groups:
-            zm.muon_step_matrices(self._hp(decay, extra_norm_sq), lst, norm_sq=norm, workspace=self._workspace)
+        for hp, (_, _, lst) in zip(configs, self._groups):
+            zm.muon_step_matrices(hp, lst, norm_sq=norm, workspace=self._workspace)
         self.t += 1
 
     def capture(self, extra_norm_sq: float = 0.0, norm_sq: Optional[torch.Tensor] = None) -> "CapturedMuonStep":

@@ -212,3 +212,21 @@ def test_refusals():
         opt.step(gradients(0)[:-1] + gradients(0, F32)[-1:])                  # two dtypes
     with pytest.raises(TypeError):
         opt.step(gradients(0), norm_sq=torch.zeros(1, device="cuda"))
+
+
+def test_a_refused_step_changes_nothing():
+    """What the calls refuse for one weight decay's matrices is refused before another's are
+    stepped: a learning rate set later, whose product with the decay does not fit
+    binary32, and a factor of it that does not."""
+    p = model()
+    opt = zs.MuonOptimizer(p, lr=1e-9, weight_decay=[0.0, 1e9, 0.0, 1e9, 0.0])
+    opt.lr = 1e30
+    before = [x.clone() for x in p + opt._momentum]
+    with pytest.raises(zs.ZShardError):
+        opt.step(gradients(0))
+    assert opt.t == 0 and all(torch.equal(x, y) for x, y in zip(before, p + opt._momentum))
+    for scale in (float("inf"), float("nan"), 1e39):
+        with pytest.raises(ValueError):
+            zs.MuonOptimizer(p, lr=0.01, weight_decay=[0.0, 0.1, 0.0, 0.1, 0.0], scale=[1.0, scale, 1.0, 1.0, 1.0])
+        with pytest.raises(ValueError):
+            zs.MuonMatrices(p, p, [torch.zeros_like(x) for x in p], scale=scale)
