@@ -124,6 +124,10 @@ class _List:
         self.tensors = {}
 
     def _set(self, field: str, ts, pointers) -> None:
+        # all on the GPU that is current now (_pointers); the list may be another one's
+        held = next((t for t in ts or () if t is not None), None)
+        if held is not None and held.device != self.device:
+            raise ValueError(f"{field}: on {held.device}, the list on {self.device}")
         self.array[field][:self.count] = pointers
         self.tensors[field] = list(ts) if ts is not None else None
 

@@ -406,3 +406,18 @@ def test_a_momentum_that_is_one_in_binary32_is_refused():
             zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, momentum=momentum))
     sc = M.MuonScalars.from_buffer_copy(zs.muon_scalars_bytes(zs.MuonConfig(lr=0.01, momentum=1.0 - 2.0 ** -24)))
     assert sc.momentum == 1.0 - 2.0 ** -24 and sc.one_minus_momentum == 2.0 ** -24
+
+
+def test_lists_refuse_tensors_of_another_device(monkeypatch):
+    """A list made while one GPU was current, given tensors while another one is: a call on the
+    first would follow addresses of the second.  (Two kinds of device stand for two GPUs.)"""
+    monkeypatch.setattr(T, "_pointers", lambda ts, *a, **k: ([FAKE] * len(ts), ts[0].dtype if ts else None))
+    x, other = torch.zeros(4, 8), torch.zeros(4, 8, device="meta")
+    muon_list, mixed, grads = zs.MuonMatrices([x], [x], [x]), zs.MixedTensors([x]), zs.GradTensors([x])
+    for call in (lambda: muon_list.set_grads([other]), lambda: mixed.set([other]), lambda: grads.set_grads([other]),
+                 lambda: zs.ProductMatrices([x], [torch.zeros(8, 4, device="meta")], [torch.zeros(4, 4)]),
+                 lambda: zs.OrthogonalizeMatrices([x], [other])):
+        with pytest.raises(ValueError, match="the list on"):
+            call()
+    for lst in (muon_list, mixed, grads):
+        assert all(t.device == x.device for ts in lst.tensors.values() for t in ts)
