@@ -46,7 +46,7 @@ Over lists of tensors (include/zshard_tensors.h), each list marshalled once:
 
 Over lists of matrices (include/zshard_matrices.h):
 
-    ProductMatrices(a, b, d, c=None) / GramMatrices(a, d, c=None) / OrthogonalizeMatrices(inputs, outputs)
+    ProductMatrices(a, b, d, c=None) / GramMatrices(a, d, c=None, transposed=None) / OrthogonalizeMatrices(inputs, outputs)
     MuonMatrices(params, grads, momenta, param_bf16=None, scale="rms")
     product_add_matrices(products, alpha=1.0, beta=1.0, workspace=None)         d = alpha op(a) op(b) + beta c
     gram_add_matrices(grams, alpha=1.0, beta=1.0, workspace=None)               d = alpha a a^T + beta c
@@ -56,7 +56,6 @@ Over lists of matrices (include/zshard_matrices.h):
 TensorOptimizer(params, lr=..., state_bits=32 or 8) orders the calls over
 tensors and MuonOptimizer(matrices, lr=...) those over matrices, as
 ShardOptimizer does the calls over a flat shard.
-
 
 DeviceArena(nbytes, device) holds one physically contiguous block of device
 memory and hands out 2 MiB-aligned views of it (ShardOptimizer(arena=...)).

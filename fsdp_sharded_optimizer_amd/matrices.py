@@ -207,20 +207,29 @@ class ProductMatrices(_MatrixList):
 
 class GramMatrices(_MatrixList):
     """The matrices of gram_add_matrices: d = a a^T + c, or a^T a + c where d has
-    a's columns as its side (of a square a: a a^T).  a: fp32 or bf16; c (a list,
-    or None) and d: one dtype.  c[k] may be d[k] itself."""
+    a's columns as its side.  transposed: for a square a both fit, and a a^T is
+    taken unless it is True (one value, or one per tensor of a; None: by d's side).
+    a: fp32 or bf16; c (a list, or None) and d: one dtype.  c[k] may be d[k] itself."""
 
-    def __init__(self, a, d, c=None):
+    def __init__(self, a, d, c=None, transposed: Union[None, bool, Sequence[Optional[bool]]] = None):
+        a = list(a)
+        asked = [transposed] * len(a) if transposed is None or np.isscalar(transposed) else list(transposed)
+        if len(asked) != len(a):
+            raise ValueError(f"transposed: {len(asked)} values for {len(a)} tensors")
+        asked = [x for t, x in zip(a, asked)
+                 for _ in range(t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 3 else 1)]
         a, d = _matrices(a, "a"), _matrices(d, "d")
         super().__init__(Gram, [tuple(t.shape) for t in d], _device(d))
         self.in_dtype = _dtype(self._put("a", "a", a, [tuple(t.shape) for t in a], _FLOATS))
         if len(a) != self.count:
             raise ValueError(f"{len(a)} a for {self.count} d")
         turned = []
-        for k, (t, s) in enumerate(zip(a, self.shapes)):
+        for k, (t, s, x) in enumerate(zip(a, self.shapes, asked)):
             if s not in ((t.shape[0],) * 2, (t.shape[1],) * 2):
                 raise ValueError(f"d[{k}]: {s} is neither side of a[{k}], {tuple(t.shape)}")
-            turned.append(int(s[0] != t.shape[0]))
+            turned.append(int(s[0] != t.shape[0]) if x is None else int(bool(x)))
+            if s[0] != t.shape[turned[-1]]:
+                raise ValueError(f"d[{k}]: {s}, but a[{k}] is {tuple(t.shape)} and transposed {bool(x)}")
         kind = self._put("d", "d", d, self.shapes, _FLOATS)
         self.d_dtype = _dtype(kind)
         if c is not None and self.count and self._put("c", "c", _matrices(c, "c"), self.shapes, _FLOATS) != kind:

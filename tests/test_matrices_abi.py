@@ -421,3 +421,17 @@ def test_lists_refuse_tensors_of_another_device(monkeypatch):
             call()
     for lst in (muon_list, mixed, grads):
         assert all(t.device == x.device for ts in lst.tensors.values() for t in ts)
+
+
+def test_the_side_of_a_square_matrixs_gram(monkeypatch):
+    monkeypatch.setattr(T, "_pointers", lambda ts, *a, **k: ([FAKE] * len(ts), ts[0].dtype if ts else None))
+    square, wide, stack, d4, d8 = (torch.zeros(s) for s in ((4, 4), (4, 8), (3, 4, 4), (4, 4), (8, 8)))
+
+    def turned(a, d, **kw):
+        return list(zs.GramMatrices(a, d, **kw).array["transposed"])
+    assert turned([square, wide, wide], [d4, d4, d8]) == [0, 0, 1]
+    assert turned([square], [d4], transposed=True) == [1] and turned([square], [d4], transposed=False) == [0]
+    assert turned([square, wide, stack], [d4, d8, torch.zeros(3, 4, 4)], transposed=[True, None, True]) == [1, 1, 1, 1, 1]
+    for a, d, kw in (([wide], [d4], True), ([wide], [d8], False), ([square], [d4], [True, False]), ([square, wide], [d4, d4], True)):
+        with pytest.raises(ValueError):
+            zs.GramMatrices(a, d, transposed=kw)
