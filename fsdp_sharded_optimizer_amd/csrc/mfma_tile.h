@@ -162,8 +162,8 @@ struct Stager {
 // acc: a tile's sums (pair_of and lane_place say where).
 //
 // One k tile in LDS is multiplied while the next STAGES - 1 ones' loads arrive.  Two
-// stages of the large tiles fill the LDS; a workgroup of small ones waits for little but
-// its loads, and has four.
+// stages of the largest tiles fill most of the LDS; a workgroup of the smallest ones
+// waits for little but its loads, and has three.
 // A tile is worked through in phases of two rows of fragments; each phase first
 // starts the LDS reads of the next one's fragments, so that they arrive behind
 // its matrix instructions.  The last phase's are in the next tile: before it

@@ -114,8 +114,8 @@ typedef struct {
  * matrix: singular values below 2^-22 of the largest are what roundings left there, and
  * grow by a each step until the polynomial holds them.
  * A zero matrix gives zeros, one with a value that is not finite NaN.  steps: 1 to
- * ZS_NS_MAX_STEPS; |a|, |b|, |c| at most 32 and such that X stays bounded (fp16 ends
- * at 255 times the scale); eps: at least 1e-30.
+ * ZS_NS_MAX_STEPS; |a|, |b|, |c| at most 32 and such that X, S and b S + c S^2 stay
+ * bounded (fp16 ends at 255 times the scale); eps: at least 1e-30.
  */
 #define ZS_NS_MAX_STEPS 32
 ZS_API int64_t orthogonalize_matrices_workspace_bytes(const zs_orthogonal* list, int32_t count);
