@@ -127,3 +127,18 @@ def test_lists_longer_than_a_table(shapes, size):
         # u is 0.0975 and 0.142625 of the gradient: of one direction, which the polynomial takes alone
         want = 2 * ref.orthogonal(g[k])
         assert ref.far(-p[k], want) <= ref.NS_BOUND + 2 ** -20, shapes[k]
+
+
+@pytest.mark.parametrize("steps", [8, 12, 32])
+def test_many_steps_stay_bounded(steps):
+    """Of matrices without full rank, short sides above 64: the polynomial keeps [0, 1.2017] in
+    itself, and brings what is up to 0.05 above back (f(1.25) = 1.18); a step is off by less.
+    The last one may leave it by what the result is off by."""
+    x = [ref.matrix(96, 200, 1, "rank one"), ref.matrix(300, 70, 2, "rank one", BF16).float(), ref.matrix(300, 500, 3, "directions"),
+         rand(128, 3, seed=4) @ rand(3, 256, seed=5), torch.ones(65, 65, device="cuda")]
+    y = [torch.empty_like(t, dtype=BF16) for t in x]
+    zs.orthogonalize_matrices(zs.OrthogonalizeMatrices(x, y), steps=steps)
+    for b in y:
+        assert torch.isfinite(b).all()
+        b = b.double()
+        assert float(torch.linalg.matrix_norm(b, 2)) <= 1.2017 + (ref.NS_BOUND + ref.BF16) * float(b.norm()), tuple(b.shape)
