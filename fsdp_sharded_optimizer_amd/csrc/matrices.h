@@ -102,11 +102,11 @@ struct NsPlace {
 // where the polynomial has no bound (3.4445: a 64 x 256 matrix of rank 8 off by 1e-4 after
 // 5 steps, 0.4 after 8, NaN after 12).  And Q, a pair, is off by 2^-22 of its own largest
 // value, a^steps there.  So X becomes Q X, and S is formed anew from it, before |a|^steps
-// passes kSkinnyGrowth, and after kSkinnySteps steps (with them Q is off by 1.2e-4 at
-// most, S by 512^2 / a^2 2^-23 = 3e-3 of what X is off the small values by).  After
-// kSkinnySteps every workgroup of the next sum of S does so for its columns (a launch that
-// only the number of steps decides on: a captured step's coefficients may change); within them,
-// for a above 3.48, the workgroup that forms Q, for all columns.
+// passes kSkinnyGrowth, and after kSkinnySteps steps: Q is off by 512 * 2^-22 = 1.2e-4 at
+// most then, and S, where X is small, by 512^2 / a^2 * 2^-23 = 3e-3.  After kSkinnySteps
+// every workgroup of the next sum of S does so for its columns (a launch that only the number
+// of steps decides on: a captured step's coefficients may change); within them, for |a| above
+// 3.48, the workgroup that forms Q, for all columns.
 constexpr int64_t kSkinny = kPadSide;
 constexpr int32_t kSkinnySteps = 5;
 constexpr float kSkinnyGrowth = 512.0f;
