@@ -455,9 +455,10 @@ int32_t run_ns(const T* list, int32_t count, int32_t in_dtype, int kind, int32_t
                 if (rc != ZS_OK) return rc;
             }
         }
-        for (int32_t done = 0; done < steps && skinny > 0; done += kSkinnySteps) {
+        const int32_t at_once = sc_dev == nullptr ? skinny_steps_at_once(sc.a) : kSkinnySteps;
+        for (int32_t done = 0; done < steps && skinny > 0; done += at_once) {
             b.which = done > 0;
-            b.steps = std::min(steps - done, kSkinnySteps);
+            b.steps = std::min(steps - done, at_once);
             rc = phase(true, [&](const Matrix& x) { return SkinnyPlace(x.n()).chunks; },
                        [&](const NsBatch& x, int64_t tiles) { return launch_skinny_gram(x, tiles, stream); });
             if (rc != ZS_OK) return rc;

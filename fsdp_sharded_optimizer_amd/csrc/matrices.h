@@ -103,13 +103,20 @@ struct NsPlace {
 // 5 steps, 0.4 after 8, NaN after 12).  And Q, a pair, is off by 2^-22 of its own largest
 // value, a^steps there.  So X becomes Q X, and S is formed anew from it, before |a|^steps
 // passes kSkinnyGrowth, and after kSkinnySteps steps: Q is off by 512 * 2^-22 = 1.2e-4 at
-// most then, and S, where X is small, by 512^2 / a^2 * 2^-23 = 3e-3.  After kSkinnySteps
-// every workgroup of the next sum of S does so for its columns (a launch that only the number
-// of steps decides on: a captured step's coefficients may change); within them, for |a| above
-// 3.48, the workgroup that forms Q, for all columns.
+// most then, and S, where X is small, by 512^2 / a^2 * 2^-23 = 3e-3.  Every workgroup of the
+// next sum of S does so for its columns.  Where a is in device memory the launches cannot
+// go by it (a captured step's coefficients may change) and are those of kSkinnySteps;
+// within them, for |a| above 3.48, the workgroup that forms Q does so for all columns,
+// which takes longer (5 steps with a = 4.08 of 64 x 11008: 114 us, so 564).
 constexpr int64_t kSkinny = kPadSide;
 constexpr int32_t kSkinnySteps = 5;
 constexpr float kSkinnyGrowth = 512.0f;
+__host__ __device__ __forceinline__ int32_t skinny_steps_at_once(float a) {
+    const float slope = a < 0.0f ? -a : a;
+    int32_t steps = 1;
+    for (float grown = slope * slope; steps < kSkinnySteps && grown <= kSkinnyGrowth; grown *= slope) ++steps;
+    return steps;
+}
 // Its place: X's first values, second values and first values again (together the
 // 192 x np right operand of Q X), the partial sums of S, Q as its left operand
 // (64 x 192), Q's scale.

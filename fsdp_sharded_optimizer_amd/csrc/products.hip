@@ -625,9 +625,7 @@ __global__ __launch_bounds__(kStepThreads) void skinny_steps_kernel(const NsBatc
         s.v[i / kSkinny * kPitch + i % kSkinny] = x * (1.0f / (kNsScale * kNsScale));
     }
     __syncthreads();
-    const float slope = fabsf(ca);
-    int at_once = 1;
-    for (float grown = slope * slope; at_once < b.steps && grown <= kSkinnyGrowth; grown *= slope) ++at_once;
+    const int at_once = skinny_steps_at_once(ca);
     int left = b.steps;
     for (; left > at_once; left -= at_once) {
         polynomials(s, t, m, q, (int)e.m, at_once, ca, cb, cc);

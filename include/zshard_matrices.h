@@ -182,7 +182,8 @@ ZS_API int32_t muon_scalars(const zs_muon* hp, zs_muon_scalars* out);
 /* muon_step_matrices with its scalars read from device memory when the kernels
  * run (8-byte aligned, must not overlap a written buffer): one captured graph
  * replays every step.  The number of Newton-Schulz steps is the launches' and
- * therefore an argument. */
+ * therefore an argument.  The coefficients are not the launches': matrices of a short side
+ * up to 64 take longer with |a| above 3.48, and come out the same to rounding. */
 ZS_API int32_t muon_step_matrices_dev(const zs_muon_scalars* scalars_dev, int32_t ns_steps, const zs_muon_matrix* list,
                                       int32_t count, int32_t param_dtype, int32_t grad_dtype, const double* norm_sq_dev,
                                       void* workspace, int64_t workspace_bytes, void* hip_stream);

@@ -111,10 +111,11 @@ def test_long_matrices(coefficients, steps):
         assert ref.far(b, ref.orthogonal(a, steps, coefficients)) <= bound, tuple(a.shape)
 
 
-@pytest.mark.parametrize("coefficients,steps", [(ref.COEFFICIENTS, 11), ((4.0848, -6.8946, 2.927), 6)])
-def test_momentum_steps_with_device_scalars_are_the_same(coefficients, steps):
-    """The launches depend on the number of steps alone, what a product covers on the
-    coefficients that the kernels read."""
+@pytest.mark.parametrize("coefficients,steps,same", [(ref.COEFFICIENTS, 11, True), ((4.0848, -6.8946, 2.927), 6, False),
+                                                     ((5.0, -20.0, 16.0), 5, False)])
+def test_momentum_steps_with_device_scalars(coefficients, steps, same):
+    """The bits of the call with host scalars; for a polynomial that takes fewer steps at a
+    time (the launches cannot go by a coefficient in device memory) both by the formula."""
     shapes = [(64, 64), (3, 500), (500, 40), (96, 80), (1, 1), (64, 3000)]
     hp = zs.MuonConfig(lr=0.02, ns_steps=steps, coefficients=coefficients)
     out = []
@@ -129,4 +130,13 @@ def test_momentum_steps_with_device_scalars_are_the_same(coefficients, steps):
         else:
             zs.muon_step_matrices(hp, lst)
         out.append(p + m)
-    assert all(torch.equal(a, b) for a, b in zip(*out))
+        for i, (r, c) in enumerate(shapes):
+            assert torch.equal(m[i], ref.momentum(torch.zeros(r, c, device="cuda"), g[i], 0.95, True)[0])
+            u = ref.momentum(torch.zeros(r, c, device="cuda"), g[i], 0.95, True)[1]
+            o, old = ref.orthogonal(u, steps, coefficients), ref.matrix(r, c, i).double()
+            want = old - 0.02 * 0.2 * max(r, c) ** 0.5 * o
+            off = growth(u, steps, coefficients) * 2.0 ** -20 + ref.NS_BOUND
+            step = 0.02 * 0.2 * max(r, c) ** 0.5 * float(o.norm())
+            if min(r, c) <= 64:
+                assert float((p[i].double() - want).norm()) <= off * step + 4 * ref.FP32 * (float(old.norm()) + step), (r, c)
+    assert all(torch.equal(a, b) for a, b in zip(*out)) or not same
